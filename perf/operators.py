@@ -240,8 +240,10 @@ def _plain_plan(s):
 
 
 def _row_scale(X, Q):
-    """fl(a / Q) and fl(Q / a) of the rows' largest magnitudes a; zeros where a is 0."""
+    """fl(a / Q) and fl(Q / a) of the rows' largest magnitudes a; zeros where a is 0.  Q is a tensor:
+    with a Python number torch multiplies by a rounded reciprocal instead of dividing."""
     a = X.abs().amax(dim=-1, keepdim=True)
+    Q = torch.full_like(a, Q)
     inv = Q / a
     zero = (a == 0) | torch.isinf(inv)
     return torch.where(zero, 0.0, a / Q), torch.where(zero, 0.0, inv)
