@@ -225,6 +225,107 @@ int damp_decode_step_validated(const damp_pool* pool, int n, const int32_t* slot
                                int gate, const float* alpha, const float* beta, float* out,
                                void* stream);
 
+/* ---- layers without the delta rule, and prompts ---------------------------
+ *
+ * Two update rules of a head with a scalar decay alpha_t per token:
+ *   DAMP_RULE_DECAY  S <- alpha_t S + k_t v_t^T
+ *   DAMP_RULE_DELTA  S <- alpha_t S;  S <- S + beta_t k_t (v_t - S^T k_t)^T
+ *                    (GDN: the rule of damp_decode_step)
+ *   out_t = S^T q_t after the update.
+ * q and k may have fewer heads than v (H_qk, a divisor of the pool's H): value
+ * head h reads q/k head h / (H / H_qk).
+ */
+#define DAMP_RULE_DELTA 0
+#define DAMP_RULE_DECAY 1
+
+/*
+ * One token of the decay rule on the pool, for every (entry b, head h):
+ *   S'_ij = fl(alpha S^_ij);  X_ij = fma(k_i, v_j, S'_ij)
+ *   out_j = sum_i q_i X_ij (FP32, any order, from X before requantization)
+ * and X requantized in place by the decode step's quantizer.  Arguments as
+ * damp_decode_step, with q, k: device [n][H_qk][d_k]; alpha: device float32
+ * [n][H].  Every pool format and shape.
+ */
+int damp_decay_step(const damp_pool* pool, int n, const int32_t* slot_idx, int in_dtype, int H_qk,
+                    const void* q, const void* k, const void* v, const float* alpha, float* out,
+                    void* stream);
+
+/*
+ * Index arrays of a ragged batch of n requests, built on the device from the
+ * requests' lengths.  One launch; build it once for a batch and use it in
+ * every layer.
+ *   lengths  : device int32 [n], tokens of each request in this batch (0: none)
+ *   past     : device int32 [n] or NULL (all zero): tokens already in the
+ *              request's state.  0: the request starts from a zero state.
+ *   slot_idx : device int32 [n], the pool slot of each request's state; < 0:
+ *              padding.  Distinct where >= 0.
+ *   max_tokens : token rows of the batch's tensors
+ * Outputs (device int32):
+ *   cu_seqlens [n + 1]  rows [cu[r], cu[r+1]) belong to request r, in order
+ *   load_slot  [n]      slot to start from (-1: zero state, or nothing to do)
+ *   store_slot [n]      slot to leave the state in (-1: nothing to do): the
+ *                       request has rows and a slot in [0, n_slots)
+ *   block_table [max_blocks][4]  {request, first token row, tokens, index in
+ *                       its request} of every block of up to DAMP_PLAN_BLOCK
+ *                       consecutive tokens, in row order; -1 behind the last.
+ *                       max_blocks from damp_plan_blocks.  16-byte aligned.
+ *   token_slot [max_tokens]  slot of each row's request (-1: padding, or a row
+ *                       behind the last request)
+ *   token_pos  [max_tokens]  past + position in its request (-1 behind the
+ *                       last).  Both token maps may be NULL; 16-byte aligned.
+ *   totals [4]          {rows, blocks, longest request, DAMP_PLAN_EFLAG_* bits}
+ * A negative length or past counts as 0 (DAMP_PLAN_EFLAG_VALUE).  A request
+ * whose rows would end behind max_tokens is dropped together with every later
+ * request that has rows (DAMP_PLAN_EFLAG_TOKENS): no rows, slots -1.  A slot
+ * >= n_slots counts as padding (DAMP_PLAN_EFLAG_SLOT).
+ * Limits: n <= DAMP_PLAN_MAX_REQUESTS, max_tokens <= DAMP_PLAN_MAX_TOKENS.
+ */
+#define DAMP_PLAN_BLOCK 64
+#define DAMP_PLAN_MAX_REQUESTS 16384
+#define DAMP_PLAN_MAX_TOKENS (1 << 24)
+#define DAMP_PLAN_EFLAG_VALUE 1
+#define DAMP_PLAN_EFLAG_TOKENS 2
+#define DAMP_PLAN_EFLAG_SLOT 4
+int damp_plan_blocks(int n, int max_tokens, int* max_blocks);
+int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const int32_t* slot_idx,
+                    int n_slots, int max_tokens, int32_t* cu_seqlens, int32_t* load_slot,
+                    int32_t* store_slot, int32_t* block_table, int32_t* token_slot,
+                    int32_t* token_pos, int32_t* totals, void* stream);
+
+/*
+ * The prompts of a planned batch through one layer: every token's readout, and
+ * every request's state left in its pool slot, ready for damp_decode_step
+ * (DAMP_RULE_DELTA) or damp_decay_step (DAMP_RULE_DECAY).
+ *   n, max_tokens, cu_seqlens, load_slot, store_slot, block_table : the plan
+ *   q, k  : device [max_tokens][H_qk][d_k], v: device [max_tokens][H][d_v],
+ *           bf16 or float32 (in_dtype), heads and channels dense; *_stride =
+ *           elements between token rows (views of one projection's output are
+ *           fine), a multiple of 16 bytes.
+ *   alpha : device float32 [max_tokens][H], >= 0 (0 forgets the state)
+ *   beta  : device float32 [max_tokens][H] (DAMP_RULE_DELTA; NULL for DECAY)
+ *   out   : device [max_tokens][H][d_v], dense, the type of q.  Rows of
+ *           requests without a slot are zeroed; rows behind the last request
+ *           are left as they were.
+ *   workspace : device, damp_prefill_workspace bytes, 256-byte aligned; not
+ *           shared by calls that may run at the same time.  NULL allowed when
+ *           that is 0.
+ * A request with load_slot >= 0 continues from that slot's state, another
+ * starts from zeros; a slot the plan does not store to keeps its bytes.  A
+ * store_slot >= n_slots sets DAMP_EFLAG_SLOT_RANGE (rows zeroed).  States are
+ * FP32 inside the call: a quantized pool's are dequantized before it and
+ * quantized once after it (damp_pool_unpack / damp_pool_pack).
+ * The readout is computed from FP32 states and rounded once to the output's
+ * type.
+ */
+int damp_prefill_workspace(const damp_pool* pool, int rule, int n, int max_tokens, int in_dtype,
+                           size_t* bytes);
+int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
+                 const int32_t* cu_seqlens, const int32_t* load_slot, const int32_t* store_slot,
+                 const int32_t* block_table, int in_dtype, int H_qk, const void* q,
+                 int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, const float* alpha, const float* beta, void* out,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Test hooks of the failure path (for tests of the library; not for serving).
  *   wait_limit_ns : bound of every internal pipeline wait of the decode step;

@@ -41,9 +41,18 @@ DAMP_GATE_SCALAR = 0
 DAMP_GATE_VECTOR = 1
 DAMP_DTYPE_BF16 = 0
 DAMP_DTYPE_F32 = 1
+DAMP_RULE_DELTA = 0
+DAMP_RULE_DECAY = 1
+DAMP_PLAN_BLOCK = 64
+DAMP_PLAN_MAX_REQUESTS = 16384
+DAMP_PLAN_MAX_TOKENS = 1 << 24
+DAMP_PLAN_EFLAG_VALUE = 1
+DAMP_PLAN_EFLAG_TOKENS = 2
+DAMP_PLAN_EFLAG_SLOT = 4
 
 FORMATS = {"fp32": DAMP_FMT_FP32, "int8": DAMP_FMT_INT8_ROW, "mixed": DAMP_FMT_MIXED,
            "fp8": DAMP_FMT_FP8_ROW}
+RULES = {"delta": DAMP_RULE_DELTA, "decay": DAMP_RULE_DECAY}
 
 
 class DampError(RuntimeError):
@@ -58,7 +67,7 @@ def _load():
             f"{LIB_PATH} is missing; build it with "
             "`python quantized_linear_attention_damp_b200/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, I, S, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
     sig = {
         "damp_status_string": (ctypes.c_char_p, [I]),
         "damp_layout": (I, [I, I, I, I, ctypes.POINTER(S), ctypes.POINTER(S)]),
@@ -85,6 +94,11 @@ def _load():
         "damp_calib_select": (I, [I, I, I, P, P, P, P]),
         "damp_calib_select_budget": (I, [I, I, I, P, P, P, P, P]),
         "damp_calib_select_budget_static": (I, [I, I, I, P, P, P, P]),
+        "damp_decay_step": (I, [P, I, P, I, I, P, P, P, P, P, P]),
+        "damp_plan_blocks": (I, [I, I, ctypes.POINTER(I)]),
+        "damp_batch_plan": (I, [I, P, P, P, I, I, P, P, P, P, P, P, P, P]),
+        "damp_prefill_workspace": (I, [P, I, I, I, I, ctypes.POINTER(S)]),
+        "damp_prefill": (I, [P, I, I, I, P, P, P, P, I, I, P, L, P, L, P, L, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -377,6 +391,191 @@ def damp_decode_step_validated(pool: int, slot_idx: torch.Tensor, q: torch.Tenso
            "damp_decode_step_validated")
 
 
+# ---------------------------------------------------------------- decay rule, prompts
+
+class _on_device:
+    """Makes the tensors' device current for a launch (a stream belongs to its
+    device); does nothing when it already is."""
+
+    def __init__(self, device):
+        i = device.index
+        self.guard = None if i is None or i == torch.cuda.current_device() \
+            else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _alloc_stream(stream, device):
+    """Context in which torch allocates (and fills) on ``stream``."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    return torch.cuda.stream(stream)
+
+
+def _in_dtype(q, k, v) -> int:
+    _cuda(q, None, "q")
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("q, k, v must be bfloat16 or float32")
+    _cuda(k, q.dtype, "k")
+    _cuda(v, q.dtype, "v")
+    return DAMP_DTYPE_BF16 if q.dtype == torch.bfloat16 else DAMP_DTYPE_F32
+
+
+def _shared_heads(q, H: int, n: int, d_k: int) -> int:
+    """Heads of q [n][H_qk][d_k]; value head h reads head h // (H // H_qk)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError(f"q must have shape ({n}, H_qk, {d_k})")
+    if q.shape[1] < 1 or H % q.shape[1]:
+        raise ValueError(f"q's heads must divide the pool's {H}, got {q.shape[1]}")
+    return q.shape[1]
+
+
+def damp_decay_step(pool: int, slot_idx: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                    v: torch.Tensor, alpha: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """One token of the decay rule, S <- alpha S + k v^T, out = S^T q.  q, k
+    [n][H_qk][d_k] (H_qk divides H) and v [n][H][d_v] in bf16 or fp32; alpha
+    fp32 [n][H]; out fp32 [n][H][d_v]; n = slot_idx.numel()."""
+    _, _, H, d_k, d_v = _pool_shape(pool)
+    if not isinstance(slot_idx, torch.Tensor) or slot_idx.dim() != 1:
+        raise ValueError("slot_idx must be a 1-D tensor")
+    n = slot_idx.numel()
+    H_qk = _shared_heads(q, H, n, d_k)
+    _shape(q, "q", (n, H_qk, d_k))
+    _shape(k, "k", (n, H_qk, d_k))
+    _shape(v, "v", (n, H, d_v))
+    _shape(alpha, "alpha", (n, H))
+    _shape(out, "out", (n, H, d_v))
+    _cuda(slot_idx, torch.int32, "slot_idx")
+    dt = _in_dtype(q, k, v)
+    _cuda(alpha, torch.float32, "alpha")
+    _cuda(out, torch.float32, "out")
+    _same_device(stream, slot_idx, q, k, v, alpha, out)
+    with _on_device(q.device):
+        _check(_lib.damp_decay_step(pool, n, _ptr(slot_idx), dt, H_qk, _ptr(q), _ptr(k), _ptr(v),
+                                    _ptr(alpha), _ptr(out), _stream(stream, q.device)),
+               "damp_decay_step")
+
+
+def damp_plan_blocks(n: int, max_tokens: int) -> int:
+    """Rows of a plan's block table."""
+    out = ctypes.c_int()
+    _check(_lib.damp_plan_blocks(n, max_tokens, ctypes.byref(out)), "damp_plan_blocks")
+    return out.value
+
+
+def damp_batch_plan(lengths: torch.Tensor, slot_idx: torch.Tensor, past, n_slots: int,
+                    max_tokens: int, cu_seqlens: torch.Tensor, load_slot: torch.Tensor,
+                    store_slot: torch.Tensor, block_table: torch.Tensor, token_slot, token_pos,
+                    totals: torch.Tensor, stream=None) -> None:
+    """Index arrays of a ragged batch from its lengths (all int32, on one
+    device).  lengths, slot_idx [n]; past [n] or None; outputs cu_seqlens
+    [n+1], load_slot [n], store_slot [n], block_table
+    [damp_plan_blocks(n, max_tokens)][4], token_slot and token_pos
+    [max_tokens] (or both None), totals [4] = rows, blocks, longest request,
+    DAMP_PLAN_EFLAG_* bits."""
+    if not isinstance(lengths, torch.Tensor) or lengths.dim() != 1:
+        raise ValueError("lengths must be a 1-D tensor")
+    n = lengths.numel()
+    blocks = damp_plan_blocks(n, max_tokens)
+    named = {"lengths": (lengths, (n,)), "slot_idx": (slot_idx, (n,)),
+             "cu_seqlens": (cu_seqlens, (n + 1,)), "load_slot": (load_slot, (n,)),
+             "store_slot": (store_slot, (n,)), "block_table": (block_table, (blocks, 4)),
+             "totals": (totals, (4,))}
+    if past is not None:
+        named["past"] = (past, (n,))
+    if token_slot is not None or token_pos is not None:
+        named["token_slot"] = (token_slot, (max_tokens,))
+        named["token_pos"] = (token_pos, (max_tokens,))
+    for name, (t, shape) in named.items():
+        _shape(t, name, shape)
+        _cuda(t, torch.int32, name)
+    _same_device(stream, *(t for t, _ in named.values()))
+    with _on_device(lengths.device):
+        _check(_lib.damp_batch_plan(n, _ptr(lengths), _ptr(past), _ptr(slot_idx), n_slots,
+                                    max_tokens, _ptr(cu_seqlens), _ptr(load_slot),
+                                    _ptr(store_slot), _ptr(block_table), _ptr(token_slot),
+                                    _ptr(token_pos), _ptr(totals),
+                                    _stream(stream, lengths.device)), "damp_batch_plan")
+
+
+def damp_prefill_workspace(pool: int, rule: int, n: int, max_tokens: int, in_dtype: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.damp_prefill_workspace(pool, rule, n, max_tokens, in_dtype, ctypes.byref(out)),
+           "damp_prefill_workspace")
+    return out.value
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the token rows of t [T][heads][d]: heads and channels
+    dense, rows anywhere."""
+    T, heads, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: heads and channels of a token row must be contiguous")
+    return t.stride(0) if T > 1 else heads * d
+
+
+def damp_prefill(pool: int, rule: int, cu_seqlens: torch.Tensor, load_slot: torch.Tensor,
+                 store_slot: torch.Tensor, block_table: torch.Tensor, q: torch.Tensor,
+                 k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor, beta, out: torch.Tensor,
+                 workspace=None, stream=None) -> None:
+    """The prompts of a planned batch through one layer (DAMP_RULE_DELTA or
+    DAMP_RULE_DECAY).  q, k [T][H_qk][d_k] and v [T][H][d_v] in bf16 or fp32,
+    token rows at any stride that is a multiple of 16 bytes; alpha fp32
+    [T][H]; beta fp32 [T][H] (delta) or None (decay); out [T][H][d_v] of q's
+    type.  ``workspace``: CUDA uint8 tensor of damp_prefill_workspace(...)
+    bytes; allocated on the call's stream when None."""
+    _, _, H, d_k, d_v = _pool_shape(pool)
+    n = load_slot.numel()
+    H_qk = _shared_heads(q, H, q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0, d_k)
+    T = q.shape[0]
+    if rule not in (DAMP_RULE_DELTA, DAMP_RULE_DECAY):
+        raise ValueError(f"unknown rule {rule}")
+    _shape(q, "q", (T, H_qk, d_k))
+    _shape(k, "k", (T, H_qk, d_k))
+    _shape(v, "v", (T, H, d_v))
+    _shape(alpha, "alpha", (T, H))
+    _shape(out, "out", (T, H, d_v))
+    dt = _in_dtype(q, k, v)
+    _cuda(alpha, torch.float32, "alpha")
+    _cuda(out, q.dtype, "out")
+    ints = (("cu_seqlens", cu_seqlens, (n + 1,)), ("load_slot", load_slot, (n,)),
+            ("store_slot", store_slot, (n,)),
+            ("block_table", block_table, (damp_plan_blocks(n, T), 4)))
+    for name, t, shape in ints:
+        _shape(t, name, shape)
+        _cuda(t, torch.int32, name)
+    if (beta is not None) != (rule == DAMP_RULE_DELTA):
+        raise ValueError("beta goes with the delta rule, and only with it")
+    if beta is not None:
+        _shape(beta, "beta", (T, H))
+        _cuda(beta, torch.float32, "beta")
+    _same_device(stream, q, k, v, alpha, out, cu_seqlens, load_slot, store_slot, block_table,
+                 *(t for t in (beta, workspace) if t is not None))
+    strides = [_token_stride(t, name) for t, name in ((q, "q"), (k, "k"), (v, "v"))]
+    with _on_device(q.device):
+        need = damp_prefill_workspace(pool, rule, n, T, dt)
+        handle = _stream(stream, q.device)
+        if workspace is not None:
+            _cuda(workspace, torch.uint8, "workspace")
+        elif need:
+            # the launch's stream owns it: the memory is given out again only
+            # behind this call's work
+            with _alloc_stream(stream, q.device):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _check(_lib.damp_prefill(pool, rule, n, T, _ptr(cu_seqlens), _ptr(load_slot),
+                                 _ptr(store_slot), _ptr(block_table), dt, H_qk, q.data_ptr(),
+                                 strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+                                 _ptr(alpha), _ptr(beta), _ptr(out), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), handle),
+               "damp_prefill")
+
+
 def damp_set_test_hooks(wait_limit_ns: int = 0, hooks: int = 0) -> None:
     """Test hooks of the failure path (process-wide): the bound of the decode
     step's internal waits (0 = default, 2 s) and DAMP_HOOK_HOLD_FIRST_ITEM."""
@@ -493,6 +692,30 @@ def damp_calib_select_budget_static(H: int, d_k: int, budget: int, acc: torch.Te
 
 # ---------------------------------------------------------------- convenience
 
+class BatchPlan:
+    """Buffers of a ragged batch's index arrays (damp_batch_plan) for up to
+    ``n`` requests and ``max_tokens`` token rows.  ``build`` fills them on the
+    device; a captured ``build`` reads the lengths its tensors hold at
+    replay."""
+
+    def __init__(self, n: int, max_tokens: int, n_slots: int, device="cuda", token_maps=True):
+        self.n, self.max_tokens, self.n_slots = n, max_tokens, n_slots
+        self.max_blocks = damp_plan_blocks(n, max_tokens)
+        e = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)  # noqa: E731
+        self.cu_seqlens, self.load_slot, self.store_slot = e(n + 1), e(n), e(n)
+        self.block_table, self.totals = e(self.max_blocks, 4), e(4)
+        self.token_slot, self.token_pos = (e(max_tokens), e(max_tokens)) if token_maps \
+            else (None, None)
+
+    def build(self, lengths: torch.Tensor, slot_idx: torch.Tensor, past=None, stream=None):
+        """Index arrays of requests with ``lengths`` tokens each, ``past``
+        tokens already in their states, and state slots ``slot_idx``."""
+        damp_batch_plan(lengths, slot_idx, past, self.n_slots, self.max_tokens, self.cu_seqlens,
+                        self.load_slot, self.store_slot, self.block_table, self.token_slot,
+                        self.token_pos, self.totals, stream)
+        return self
+
+
 class DampPool:
     """A pool buffer (allocated by PyTorch) bound to a libdamp descriptor.
 
@@ -572,6 +795,25 @@ class DampPool:
             damp_validate_slots(slot_idx, self.n_slots)
         f = damp_decode_step_validated if check_inputs else damp_decode_step
         f(self.handle, slot_idx, q, k, v, alpha, beta, out, stream)
+
+    def decay_step(self, slot_idx, q, k, v, alpha, out, stream=None):
+        """One token of the decay rule (damp_decay_step)."""
+        damp_decay_step(self.handle, slot_idx, q, k, v, alpha, out, stream)
+
+    def prefill(self, plan, q, k, v, alpha, beta=None, out=None, rule="delta", workspace=None,
+                stream=None) -> torch.Tensor:
+        """The prompts of a built BatchPlan through one layer (damp_prefill);
+        returns ``out`` (allocated, zero-filled, when None)."""
+        if plan.n_slots > self.n_slots:
+            raise ValueError(f"the plan allows slots up to {plan.n_slots}, the pool has "
+                             f"{self.n_slots}")
+        if out is None:
+            with _alloc_stream(stream, v.device):
+                out = torch.zeros_like(v, memory_format=torch.contiguous_format)
+        damp_prefill(self.handle, RULES[rule] if isinstance(rule, str) else rule, plan.cu_seqlens,
+                     plan.load_slot, plan.store_slot, plan.block_table, q, k, v, alpha, beta, out,
+                     workspace, stream)
+        return out
 
     def get_error(self, clear=False, stream=None) -> int:
         return damp_pool_get_error(self.handle, clear, stream, self.buf.device)

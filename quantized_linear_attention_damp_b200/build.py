@@ -23,7 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdamp.so")
 SOURCES = ["damp_abi.cu", "damp_decode.cu", "damp_decode_unit.cu", "damp_decode_any.cu",
-           "damp_codec.cu", "damp_calib.cu"]
+           "damp_codec.cu", "damp_calib.cu", "damp_plan.cu", "damp_decay_step.cu",
+           "damp_prefill.cu"]
 HEADERS = ["damp_internal.h", "damp_device.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -446,6 +446,200 @@ int damp_decode_step_validated(const damp_pool* pool, int n, const int32_t* slot
     return decode_common(pool, n, slot_idx, in_dtype, q, k, v, gate, alpha, beta, out, stream, 1);
 }
 
+static int shared_heads_ok(int H, int H_qk) { return H_qk >= 1 && H_qk <= H && H % H_qk == 0; }
+
+int damp_decay_step(const damp_pool* pool, int n, const int32_t* slot_idx, int in_dtype, int H_qk,
+                    const void* q, const void* k, const void* v, const float* alpha, float* out,
+                    void* stream) {
+    if (!pool || n < 0 || !pool->d.dev_buf) return DAMP_ERR_INVALID_ARGUMENT;
+    const PoolDesc& d = pool->d;
+    if (in_dtype != DAMP_DTYPE_BF16 && in_dtype != DAMP_DTYPE_F32) return DAMP_ERR_INVALID_ARGUMENT;
+    if (!shared_heads_ok(d.H, H_qk)) return DAMP_ERR_INVALID_ARGUMENT;
+    if (n == 0) return DAMP_OK;
+    if (!slot_idx || !q || !k || !v || !alpha || !out) return DAMP_ERR_INVALID_ARGUMENT;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+        return DAMP_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(slot_idx) & 3u) || (reinterpret_cast<uintptr_t>(alpha) & 3u))
+        return DAMP_ERR_MISALIGNED;
+    if ((size_t)n * d.H > (size_t)0x7fffffff) return DAMP_ERR_UNSUPPORTED;
+    damp::StepArgs a{};
+    a.d_k = d.d_k;
+    a.d_v = d.d_v;
+    a.format = d.format;
+    a.blocks = d.dev_buf + d.header_bytes;
+    a.masks = reinterpret_cast<const uint32_t*>(d.dev_buf + damp::kStatusBytes);
+    a.dir = reinterpret_cast<const uint32_t*>(d.dev_buf + d.dir_off);
+    a.status = reinterpret_cast<uint32_t*>(d.dev_buf);
+    a.slot_idx = slot_idx;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.alpha = alpha;
+    a.out = out;
+    a.n = n;
+    a.H = d.H;
+    a.n_slots = d.n_slots;
+    a.heads = reinterpret_cast<const uint4*>(d.dev_buf + d.head_off);
+    a.slot_stride = d.slot_stride;
+    return cuda_status(
+        damp::launch_decay_step(a, in_dtype, H_qk, static_cast<cudaStream_t>(stream)));
+}
+
+int damp_plan_blocks(int n, int max_tokens, int* max_blocks) {
+    if (!max_blocks || n < 0 || max_tokens < 0) return DAMP_ERR_INVALID_ARGUMENT;
+    if (n > DAMP_PLAN_MAX_REQUESTS || max_tokens > DAMP_PLAN_MAX_TOKENS)
+        return DAMP_ERR_UNSUPPORTED;
+    *max_blocks = (int)(((long long)max_tokens + (long long)(DAMP_PLAN_BLOCK - 1) * n) /
+                        DAMP_PLAN_BLOCK);
+    return DAMP_OK;
+}
+
+int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const int32_t* slot_idx,
+                    int n_slots, int max_tokens, int32_t* cu_seqlens, int32_t* load_slot,
+                    int32_t* store_slot, int32_t* block_table, int32_t* token_slot,
+                    int32_t* token_pos, int32_t* totals, void* stream) {
+    damp::PlanArgs a{};
+    const int rc = damp_plan_blocks(n, max_tokens, &a.max_blocks);
+    if (rc) return rc;
+    if (n_slots < 1 || !cu_seqlens || !totals || (!token_slot) != (!token_pos))
+        return DAMP_ERR_INVALID_ARGUMENT;
+    if (n > 0 && (!lengths || !slot_idx || !load_slot || !store_slot))
+        return DAMP_ERR_INVALID_ARGUMENT;
+    if (a.max_blocks > 0 && !block_table) return DAMP_ERR_INVALID_ARGUMENT;
+    if (!aligned16(block_table) || !aligned16(token_slot) || !aligned16(token_pos))
+        return DAMP_ERR_MISALIGNED;
+    const void* words[] = {lengths, past, slot_idx, cu_seqlens, load_slot, store_slot, totals};
+    for (const void* w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return DAMP_ERR_MISALIGNED;
+    a.lengths = lengths;
+    a.past = past;
+    a.slot_idx = slot_idx;
+    a.n = n;
+    a.n_slots = n_slots;
+    a.max_tokens = max_tokens;
+    a.cu_seqlens = cu_seqlens;
+    a.load_slot = load_slot;
+    a.store_slot = store_slot;
+    a.block_table = block_table;
+    a.token_slot = token_slot;
+    a.token_pos = token_pos;
+    a.totals = totals;
+    return cuda_status(damp::launch_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of a prefill: the FP32 states of the batch (pools whose blocks are
+// not FP32), then whatever the chosen kernels need.
+struct PrefillSpace {
+    size_t states = 0, total = 0;
+};
+
+int prefill_space(const damp_pool* pool, int rule, int n, int max_tokens, int in_dtype,
+                  PrefillSpace* w) {
+    if (!pool || n < 0 || max_tokens < 0) return DAMP_ERR_INVALID_ARGUMENT;
+    if (rule != DAMP_RULE_DELTA && rule != DAMP_RULE_DECAY) return DAMP_ERR_INVALID_ARGUMENT;
+    if (in_dtype != DAMP_DTYPE_BF16 && in_dtype != DAMP_DTYPE_F32) return DAMP_ERR_INVALID_ARGUMENT;
+    const PoolDesc& d = pool->d;
+    if (n > DAMP_PLAN_MAX_REQUESTS || max_tokens > DAMP_PLAN_MAX_TOKENS || d.H > 65535)
+        return DAMP_ERR_UNSUPPORTED;
+    if (d.format != DAMP_FMT_FP32)
+        w->states = align_up((size_t)n * d.H * d.d_k * d.d_v * 4, 256);
+    w->total = w->states;
+    return DAMP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int damp_prefill_workspace(const damp_pool* pool, int rule, int n, int max_tokens, int in_dtype,
+                           size_t* bytes) {
+    PrefillSpace w;
+    if (!bytes) return DAMP_ERR_INVALID_ARGUMENT;
+    const int rc = prefill_space(pool, rule, n, max_tokens, in_dtype, &w);
+    if (rc) return rc;
+    *bytes = w.total;
+    return DAMP_OK;
+}
+
+int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
+                 const int32_t* cu_seqlens, const int32_t* load_slot, const int32_t* store_slot,
+                 const int32_t* block_table, int in_dtype, int H_qk, const void* q,
+                 int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, const float* alpha, const float* beta, void* out,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    PrefillSpace w;
+    int rc = prefill_space(pool, rule, n, max_tokens, in_dtype, &w);
+    if (rc) return rc;
+    const PoolDesc& d = pool->d;
+    if (!d.dev_buf || !shared_heads_ok(d.H, H_qk)) return DAMP_ERR_INVALID_ARGUMENT;
+    const bool delta = rule == DAMP_RULE_DELTA;
+    if (n == 0 || max_tokens == 0) return DAMP_OK;
+    if (!cu_seqlens || !load_slot || !store_slot || !block_table || !q || !k || !v || !alpha ||
+        !out || delta != (beta != nullptr))
+        return DAMP_ERR_INVALID_ARGUMENT;
+    const int esz = in_dtype == DAMP_DTYPE_BF16 ? 2 : 4;
+    if (q_stride < (int64_t)H_qk * d.d_k || k_stride < (int64_t)H_qk * d.d_k ||
+        v_stride < (int64_t)d.H * d.d_v)
+        return DAMP_ERR_INVALID_ARGUMENT;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+        !aligned16(block_table) || (q_stride * esz) % 16 || (k_stride * esz) % 16 ||
+        (v_stride * esz) % 16)
+        return DAMP_ERR_MISALIGNED;
+    const void* words[] = {cu_seqlens, load_slot, store_slot, alpha, beta};
+    for (const void* p : words)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return DAMP_ERR_MISALIGNED;
+    if (w.total) {
+        if (!workspace) return DAMP_ERR_INVALID_ARGUMENT;
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u) return DAMP_ERR_MISALIGNED;
+        if (workspace_bytes < w.total) return DAMP_ERR_BUFFER_TOO_SMALL;
+    }
+    damp::PrefillArgs a{};
+    a.cu_seqlens = cu_seqlens;
+    a.load_slot = load_slot;
+    a.store_slot = store_slot;
+    a.block_table = block_table;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.out = out;
+    a.status = reinterpret_cast<uint32_t*>(d.dev_buf);
+    a.n = n;
+    a.max_tokens = max_tokens;
+    a.H = d.H;
+    a.H_qk = H_qk;
+    a.d_k = d.d_k;
+    a.d_v = d.d_v;
+    a.n_slots = d.n_slots;
+    a.delta = delta;
+    a.bf16 = in_dtype == DAMP_DTYPE_BF16;
+    const unsigned long long wait = g_wait_ns.load(std::memory_order_relaxed);
+    a.wait_ns = wait ? wait : damp::kDefaultWaitNs;
+    a.work = static_cast<uint8_t*>(workspace) + w.states;
+    damp_plan_blocks(n, max_tokens, &a.max_blocks);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (d.format == DAMP_FMT_FP32) {
+        a.state = d.dev_buf + d.header_bytes;
+        a.state_stride = d.slot_stride;
+        a.state_by_slot = 1;
+        return cuda_status(damp::launch_prefill_tokens(a, s));
+    }
+    a.state = static_cast<uint8_t*>(workspace);
+    a.state_stride = (unsigned long long)d.H * d.d_k * d.d_v * 4;
+    float* states = static_cast<float*>(workspace);
+    if ((rc = damp_pool_unpack(pool, n, load_slot, states, stream))) return rc;
+    if ((rc = cuda_status(damp::launch_prefill_tokens(a, s)))) return rc;
+    return damp_pool_pack(pool, n, store_slot, states, stream);
+}
+
 int damp_set_test_hooks(uint64_t wait_limit_ns, uint32_t hooks) {
     if (hooks & ~DAMP_HOOK_HOLD_FIRST_ITEM) return DAMP_ERR_INVALID_ARGUMENT;
     g_wait_ns.store(wait_limit_ns, std::memory_order_relaxed);
