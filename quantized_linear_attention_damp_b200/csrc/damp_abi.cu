@@ -227,6 +227,8 @@ int create_common(int format, int n_slots, int H, int d_k, int d_v, int hp_rows,
         }
         cudaError_t e = cudaMemcpy(dev_buf, hdr.data(), hdr.size(), cudaMemcpyHostToDevice);
         if (e == cudaSuccess) e = damp::prepare_decode(d);
+        if (e == cudaSuccess) e = damp::prepare_plan();
+        if (e == cudaSuccess && d.d_k == 128 && d.d_v == 128) e = damp::prepare_prefill();
         if (e != cudaSuccess) {
             delete[] p->d.host_masks;
             delete[] p->d.host_heads;
@@ -535,6 +537,7 @@ namespace {
 // not FP32), then whatever the chosen kernels need.
 struct PrefillSpace {
     size_t states = 0, total = 0;
+    bool chunked = false;
 };
 
 int prefill_space(const damp_pool* pool, int rule, int n, int max_tokens, int in_dtype,
@@ -547,7 +550,12 @@ int prefill_space(const damp_pool* pool, int rule, int n, int max_tokens, int in
         return DAMP_ERR_UNSUPPORTED;
     if (d.format != DAMP_FMT_FP32)
         w->states = align_up((size_t)n * d.H * d.d_k * d.d_v * 4, 256);
-    w->total = w->states;
+    w->chunked = damp::prefill_chunk_fits(d.d_k, d.d_v, in_dtype == DAMP_DTYPE_BF16);
+    int blocks = 0;
+    damp_plan_blocks(n, max_tokens, &blocks);
+    w->total = w->states + (w->chunked ? damp::prefill_chunk_bytes(n, d.H, blocks,
+                                                                   rule == DAMP_RULE_DELTA)
+                                       : 0);
     return DAMP_OK;
 }
 
@@ -626,17 +634,18 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
     a.work = static_cast<uint8_t*>(workspace) + w.states;
     damp_plan_blocks(n, max_tokens, &a.max_blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto launch = w.chunked ? damp::launch_prefill_chunk : damp::launch_prefill_tokens;
     if (d.format == DAMP_FMT_FP32) {
         a.state = d.dev_buf + d.header_bytes;
         a.state_stride = d.slot_stride;
         a.state_by_slot = 1;
-        return cuda_status(damp::launch_prefill_tokens(a, s));
+        return cuda_status(launch(a, s));
     }
     a.state = static_cast<uint8_t*>(workspace);
     a.state_stride = (unsigned long long)d.H * d.d_k * d.d_v * 4;
     float* states = static_cast<float*>(workspace);
     if ((rc = damp_pool_unpack(pool, n, load_slot, states, stream))) return rc;
-    if ((rc = cuda_status(damp::launch_prefill_tokens(a, s)))) return rc;
+    if ((rc = cuda_status(launch(a, s)))) return rc;
     return damp_pool_pack(pool, n, store_slot, states, stream);
 }
 

@@ -170,6 +170,13 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
 cudaError_t launch_decay_step(const StepArgs& a, int in_dtype, int H_qk, cudaStream_t stream);
 // Prompts, token by token (damp_prefill.cu): every shape and input type.
 cudaError_t launch_prefill_tokens(const PrefillArgs& a, cudaStream_t stream);
+// Prompts in blocks of 64 tokens on the tensor cores (damp_prefill_chunk.cu):
+// bf16 inputs, 128 x 128 states.  prepare_prefill sets the kernels' attributes
+// (damp_pool_create calls it, outside any stream capture).
+cudaError_t prepare_prefill();
+bool prefill_chunk_fits(int d_k, int d_v, int bf16);
+size_t prefill_chunk_bytes(int n, int H, int max_blocks, int delta);
+cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t stream);
 
 // Launchers (damp_decode.cu, damp_codec.cu, damp_calib.cu).  They return cudaError_t.
 cudaError_t launch_decode_step(const PoolDesc& p, const StepArgs& a, int in_dtype, int gate,

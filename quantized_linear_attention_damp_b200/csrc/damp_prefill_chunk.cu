@@ -1,0 +1,802 @@
+// damp_prefill_chunk.cu -- prompts in blocks of 64 tokens on the 5th-generation
+// tensor cores (bf16 inputs, d_k = d_v = 128), both rules.
+//
+// With gamma_t the product of a block's decays up to token t, Gamma_ts =
+// gamma_t / gamma_s, and S the state before the block (rows of Q, K, V are
+// tokens):
+//   delta rule:  (I + A) U = diag(beta) (V - diag(gamma) K S),
+//                A_ts = beta_t Gamma_ts k_t.k_s  (s < t)
+//                O  = diag(gamma) Q S + (Q K^T o Gamma) U       (s <= t)
+//                S <- gamma_C S + K^T diag(gamma_C / gamma) U
+//   decay rule:  the same with U = V.
+// Two kernels:
+//   prepare (one CTA per block and head, no order between blocks): everything
+//     that does not depend on S.  T' = (I + A)^-1 diag(beta), then
+//     G = (Q K^T o Gamma) T' and T~ = diag(gamma_C / gamma) T', so that with
+//     R = V - diag(gamma) K S:  O = diag(gamma) Q S + G R and
+//     S <- gamma_C S + K^T (T~ R).  The decay rule needs P = Q K^T o Gamma.
+//   chain (one CTA per request and head, blocks in order): the products with
+//     S, transposed so that the 128 value columns are the M dimension of every
+//     matrix instruction and S^T, R^T and U~^T = (T~ R)^T are A operands in
+//     TMEM.  S itself stays in TMEM in FP32 from the first block to the last.
+//
+// Precision: Q, K and V enter as the bf16 they are.  Every FP32 operand (S, R,
+// U~, T~, G, P) enters as a pair of bf16 values, hi + lo, which leaves 2^-17
+// of it; products of two pairs drop lo * lo.  Accumulation is FP32.
+//
+// Decays are running products, never quotients or exponentials of sums: a
+// decay of zero inside a block, or products that underflow, need no care.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "damp.h"
+#include "damp_tcgen05.cuh"
+
+namespace damp {
+namespace {
+
+constexpr int C = DAMP_PLAN_BLOCK;     // tokens of a block
+constexpr int D = 128;                 // d_k = d_v
+static_assert(C == 64, "the kernels' tiles are 64 tokens");
+
+// What the prepare kernel leaves for one (block, head), as the shared-memory
+// image the chain kernel copies: C x C bf16 matrices with 128-byte rows
+// (K-major, 128-byte swizzle), then gamma_t and gamma_C / gamma_t as FP32.
+constexpr int kMat = C * C * 2;                                  // 8192
+template <bool DELTA>
+struct Rec {
+    static constexpr int th = 0, tl = kMat;                      // T~ hi, lo (delta)
+    static constexpr int gh = DELTA ? 2 * kMat : 0, gl = gh + kMat;   // G (or P) hi, lo
+    static constexpr int gam = gl + kMat, w = gam + 4 * C;
+    static constexpr int bytes = w + 4 * C;
+};
+
+__device__ __forceinline__ uint32_t swz(int row, int byte) {     // byte in 0..127 of a 128-byte row
+    return (uint32_t)(row * 128 + (byte ^ ((row & 7) << 4)));
+}
+
+struct ChunkArgs {
+    PrefillArgs p;
+    int32_t* first_block;      // [n] index of each request's first block
+    uint8_t* records;          // [max_blocks][H] Rec
+};
+
+// ------------------------------------------------------------------ prepare
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kPrepThreads = 128;
+constexpr int kRowB = (D + 8) * 2;     // bytes of a staged Q or K row (8 extra values: no bank conflicts)
+constexpr int kF = C + 8;              // floats of a row of the FP32 matrices
+constexpr int kTB = (C + 8) * 2;       // bytes of a row of the bf16 T'
+
+template <bool DELTA>
+struct PrepSmem {
+    static constexpr int k = 0, q = C * kRowB;
+    static constexpr int img = 0;                                  // over k and q, once they are used up
+    static constexpr int dec = 2 * C * kRowB;                      // Gamma, FP32 [C][kF]
+    static constexpr int tb = dec;                                 // T' hi, lo (bf16), over Gamma
+    static constexpr int a = dec + C * kF * 4;                     // A, FP32
+    static constexpr int t = a + (DELTA ? C * kF * 4 : 0);         // (I + A)^-1, FP32
+    static constexpr int vec = t + (DELTA ? C * kF * 4 : 0);       // alpha, beta, gamma, w
+    static constexpr int bytes = vec + 4 * C * 4;
+    static_assert(Rec<DELTA>::bytes <= 2 * C * kRowB, "image fits over k and q");
+    static_assert(2 * C * kTB <= C * kF * 4, "T' fits over Gamma");
+};
+
+template <bool DELTA>
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const ChunkArgs ca) {
+    using S = PrepSmem<DELTA>;
+    using R = Rec<DELTA>;
+    const PrefillArgs& a = ca.p;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blk = blockIdx.x, h = blockIdx.y;
+    const int4 row = __ldg(reinterpret_cast<const int4*>(a.block_table) + blk);
+    const int req = row.x, t0 = row.y, len = row.z;
+    if (req < 0 || req >= a.n || t0 < 0 || len < 1 || len > C || t0 > a.max_tokens - len) return;
+    if (h == 0 && row.w == 0 && tid == 0) ca.first_block[req] = blk;
+    const int slot = __ldg(a.store_slot + req);
+    if (slot < 0 || slot >= a.n_slots) return;
+    const int hq = h / (a.H / a.H_qk);
+    float* s_dec = reinterpret_cast<float*>(sm + S::dec);
+    float* s_al = reinterpret_cast<float*>(sm + S::vec);
+    float* s_be = s_al + C;
+    float* s_ga = s_al + 2 * C;
+    float* s_w = s_al + 3 * C;
+
+    // ---- Q and K rows (zeros behind the request's end), decays
+    const uint16_t* qg = static_cast<const uint16_t*>(a.q) + (size_t)t0 * a.q_stride + (size_t)hq * D;
+    const uint16_t* kg = static_cast<const uint16_t*>(a.k) + (size_t)t0 * a.k_stride + (size_t)hq * D;
+#pragma unroll
+    for (int i = 0; i < C * (D / 8) / kPrepThreads; ++i) {
+        const int e = tid + i * kPrepThreads, r = e / (D / 8), c = e % (D / 8);
+        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
+        if (r < len) {
+            kv = __ldg(reinterpret_cast<const uint4*>(kg + (size_t)r * a.k_stride) + c);
+            qv = __ldg(reinterpret_cast<const uint4*>(qg + (size_t)r * a.q_stride) + c);
+        }
+        *reinterpret_cast<uint4*>(sm + S::k + r * kRowB + c * 16) = kv;
+        *reinterpret_cast<uint4*>(sm + S::q + r * kRowB + c * 16) = qv;
+    }
+    if (tid < C) {
+        s_al[tid] = tid < len ? __ldg(a.alpha + (size_t)(t0 + tid) * a.H + h) : 1.f;
+        if (DELTA) s_be[tid] = tid < len ? __ldg(a.beta + (size_t)(t0 + tid) * a.H + h) : 0.f;
+    }
+    __syncthreads();
+    // thread s: Gamma_ts down column s; thread C: gamma_t
+    if (tid < C) {
+        float x = 1.f;
+        s_dec[tid * kF + tid] = 1.f;
+        for (int t = tid + 1; t < C; ++t) {
+            x *= s_al[t];
+            s_dec[t * kF + tid] = x;
+        }
+        s_w[tid] = x;
+    } else if (tid == C) {
+        float x = 1.f;
+        for (int t = 0; t < C; ++t) {
+            x *= s_al[t];
+            s_ga[t] = x;
+        }
+    }
+
+    // ---- Q K^T and K K^T: warp w has rows [16 w, 16 w + 16), columns up to its diagonal
+    const uint32_t base = smem_u32(sm);
+    const int r0 = warp * 16, g = lane >> 2, c2 = (lane & 3) * 2;
+    float P[8][4], M[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) P[j][i] = M[j][i] = 0.f;
+    const uint32_t a_off = (r0 + (lane & 15)) * kRowB + (lane >> 4) * 16;
+    const uint32_t b_off = ((lane & 7) + (lane >> 4) * 8) * kRowB + ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t qa[4], ka[4];
+        ldsm4(qa, base + S::q + a_off + ks * 32);
+        if (DELTA) ldsm4(ka, base + S::k + a_off + ks * 32);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {      // two column tiles at a time
+            if (j > warp) break;
+            uint32_t b[4];
+            ldsm4(b, base + S::k + j * 16 * kRowB + b_off + ks * 32);
+            mma16816(P[2 * j], qa, b[0], b[1]);
+            mma16816(P[2 * j + 1], qa, b[2], b[3]);
+            if (DELTA) {
+                mma16816(M[2 * j], ka, b[0], b[1]);
+                mma16816(M[2 * j + 1], ka, b[2], b[3]);
+            }
+        }
+    }
+    __syncthreads();                       // Gamma is there; Q and K are used up
+
+    // ---- P = Q K^T o Gamma, A = diag(beta) K K^T o Gamma below the diagonal
+    float* s_a = reinterpret_cast<float*>(sm + S::a);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = r0 + g + (i >> 1) * 8, s = 8 * j + c2 + (i & 1);
+            const bool seen = s <= t && t < len;
+            const float dec = seen ? s_dec[t * kF + s] : 0.f;
+            P[j][i] = seen ? P[j][i] * dec : 0.f;
+            if (DELTA) s_a[t * kF + s] = s < t && t < len ? s_be[t] * (M[j][i] * dec) : 0.f;
+        }
+
+    uint8_t* img = sm + S::img;
+    if constexpr (DELTA) {
+        float* s_t = reinterpret_cast<float*>(sm + S::t);
+        __syncthreads();
+        // ---- (I + A)^-1, lower triangle: the four 16 x 16 diagonal blocks by
+        // substitution (lane = column), then pairs of blocks, then halves:
+        // the block below the diagonal is -T22 (A21 T11).  The unused upper
+        // blocks hold A21 T11.
+        if (lane < 16) {
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float v = i == lane ? 1.f : 0.f;
+                const float* ar = s_a + (r0 + i) * kF + r0;
+#pragma unroll
+                for (int k = 0; k < i; ++k) v = __fmaf_rn(-ar[k], x[k], v);
+                x[i] = v;
+                s_t[(r0 + i) * kF + r0 + lane] = v;
+            }
+        }
+        __syncthreads();
+        {
+            const int m = (tid >> 6) * 32, i = (tid & 63) >> 2, j = (tid & 3) * 4;
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float av = s_a[(m + 16 + i) * kF + m + k];
+                const float4 tv = *reinterpret_cast<const float4*>(&s_t[(m + k) * kF + m + j]);
+                x[0] = __fmaf_rn(av, tv.x, x[0]);
+                x[1] = __fmaf_rn(av, tv.y, x[1]);
+                x[2] = __fmaf_rn(av, tv.z, x[2]);
+                x[3] = __fmaf_rn(av, tv.w, x[3]);
+            }
+            *reinterpret_cast<float4*>(&s_t[(m + i) * kF + m + 16 + j]) =
+                make_float4(x[0], x[1], x[2], x[3]);
+            __syncthreads();
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float av = -s_t[(m + 16 + i) * kF + m + 16 + k];
+                const float4 tv = *reinterpret_cast<const float4*>(&s_t[(m + k) * kF + m + 16 + j]);
+                y[0] = __fmaf_rn(av, tv.x, y[0]);
+                y[1] = __fmaf_rn(av, tv.y, y[1]);
+                y[2] = __fmaf_rn(av, tv.z, y[2]);
+                y[3] = __fmaf_rn(av, tv.w, y[3]);
+            }
+            *reinterpret_cast<float4*>(&s_t[(m + 16 + i) * kF + m + j]) =
+                make_float4(y[0], y[1], y[2], y[3]);
+            __syncthreads();
+            // the scratch above the diagonal is zero for the next level
+            *reinterpret_cast<float4*>(&s_t[(m + i) * kF + m + 16 + j]) =
+                make_float4(0.f, 0.f, 0.f, 0.f);
+            // (and the diagonal blocks' own upper triangles are zeros of the substitution)
+            __syncthreads();
+        }
+        {
+            const int i = tid >> 2, j = (tid & 3) * 8;
+            float x[8] = {};
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float av = s_a[(32 + i) * kF + k];
+                const float4 t1 = *reinterpret_cast<const float4*>(&s_t[k * kF + j]);
+                const float4 t2 = *reinterpret_cast<const float4*>(&s_t[k * kF + j + 4]);
+                x[0] = __fmaf_rn(av, t1.x, x[0]);
+                x[1] = __fmaf_rn(av, t1.y, x[1]);
+                x[2] = __fmaf_rn(av, t1.z, x[2]);
+                x[3] = __fmaf_rn(av, t1.w, x[3]);
+                x[4] = __fmaf_rn(av, t2.x, x[4]);
+                x[5] = __fmaf_rn(av, t2.y, x[5]);
+                x[6] = __fmaf_rn(av, t2.z, x[6]);
+                x[7] = __fmaf_rn(av, t2.w, x[7]);
+            }
+            *reinterpret_cast<float4*>(&s_t[i * kF + 32 + j]) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(&s_t[i * kF + 36 + j]) = make_float4(x[4], x[5], x[6], x[7]);
+            __syncthreads();
+            float y[8] = {};
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float av = -s_t[(32 + i) * kF + 32 + k];
+                const float4 t1 = *reinterpret_cast<const float4*>(&s_t[k * kF + 32 + j]);
+                const float4 t2 = *reinterpret_cast<const float4*>(&s_t[k * kF + 36 + j]);
+                y[0] = __fmaf_rn(av, t1.x, y[0]);
+                y[1] = __fmaf_rn(av, t1.y, y[1]);
+                y[2] = __fmaf_rn(av, t1.z, y[2]);
+                y[3] = __fmaf_rn(av, t1.w, y[3]);
+                y[4] = __fmaf_rn(av, t2.x, y[4]);
+                y[5] = __fmaf_rn(av, t2.y, y[5]);
+                y[6] = __fmaf_rn(av, t2.z, y[6]);
+                y[7] = __fmaf_rn(av, t2.w, y[7]);
+            }
+            *reinterpret_cast<float4*>(&s_t[(32 + i) * kF + j]) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4*>(&s_t[(32 + i) * kF + 4 + j]) = make_float4(y[4], y[5], y[6], y[7]);
+            __syncthreads();
+        }
+        // ---- T' = T diag(beta) as bf16 pairs for the product below, and T~ = diag(w) T' into the
+        // image.  Rows behind the end: beta is zero, so their columns vanish; their rows may not
+        // (nothing reads U there, but K's rows are zero as well).
+        for (int e = tid; e < C * C / 2; e += kPrepThreads) {
+            const int t = e / (C / 2), s = e % (C / 2) * 2;
+            const float2 tv = *reinterpret_cast<const float2*>(&s_t[t * kF + s]);
+            const float x = s <= t ? tv.x * s_be[s] : 0.f, y = s + 1 <= t ? tv.y * s_be[s + 1] : 0.f;
+            uint32_t hi, lo;
+            split_bf16(x, y, hi, lo);
+            *reinterpret_cast<uint32_t*>(sm + S::tb + t * kTB + s * 2) = hi;
+            *reinterpret_cast<uint32_t*>(sm + S::tb + C * kTB + t * kTB + s * 2) = lo;
+            split_bf16(s_w[t] * x, s_w[t] * y, hi, lo);
+            *reinterpret_cast<uint32_t*>(img + R::th + swz(t, s * 2)) = hi;
+            *reinterpret_cast<uint32_t*>(img + R::tl + swz(t, s * 2)) = lo;
+        }
+        __syncthreads();
+        // ---- G = P T', over the k steps and column tiles the triangles leave
+        float G[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) G[j][i] = 0.f;
+        const uint32_t t_off = base + S::tb + (lane & 15) * kTB + (lane >> 4) * 16;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            if (ks > warp) break;
+            uint32_t ph[4], pl[4];
+            split_bf16(P[2 * ks][0], P[2 * ks][1], ph[0], pl[0]);
+            split_bf16(P[2 * ks][2], P[2 * ks][3], ph[1], pl[1]);
+            split_bf16(P[2 * ks + 1][0], P[2 * ks + 1][1], ph[2], pl[2]);
+            split_bf16(P[2 * ks + 1][2], P[2 * ks + 1][3], ph[3], pl[3]);
+#pragma unroll
+            for (int j = 0; j <= ks; ++j) {
+                uint32_t bh[4], bl[4];
+                ldsm4t(bh, t_off + ks * 16 * kTB + j * 32);
+                ldsm4t(bl, t_off + C * kTB + ks * 16 * kTB + j * 32);
+                mma16816(G[2 * j], ph, bh[0], bh[1]);
+                mma16816(G[2 * j + 1], ph, bh[2], bh[3]);
+                mma16816(G[2 * j], pl, bh[0], bh[1]);
+                mma16816(G[2 * j + 1], pl, bh[2], bh[3]);
+                mma16816(G[2 * j], ph, bl[0], bl[1]);
+                mma16816(G[2 * j + 1], ph, bl[2], bl[3]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) P[j][i] = G[j][i];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t hi, lo;
+            split_bf16(P[j][2 * i], P[j][2 * i + 1], hi, lo);
+            const uint32_t at = swz(r0 + g + 8 * i, (8 * j + c2) * 2);
+            *reinterpret_cast<uint32_t*>(img + R::gh + at) = hi;
+            *reinterpret_cast<uint32_t*>(img + R::gl + at) = lo;
+        }
+    if (tid < C) {
+        reinterpret_cast<float*>(img + R::gam)[tid] = s_ga[tid];
+        reinterpret_cast<float*>(img + R::w)[tid] = s_w[tid];
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+        bulk_s2g(ca.records + ((size_t)blk * a.H + h) * R::bytes, smem_u32(img), R::bytes);
+        bulk_commit();
+        bulk_wait_all<0>();
+    }
+}
+
+// ------------------------------------------------------------------ chain
+
+constexpr int kChainThreads = 320;     // 8 compute warps, the loader, the issuer of matrix instructions
+constexpr int kComputeWarps = 8;
+constexpr int kStages = 2;
+constexpr int kTile = C * D * 2;       // bytes of a Q, K or V tile: two halves of 64 channels
+constexpr int kHalf = kTile / 2;
+
+template <bool DELTA>
+struct ChainSmem {
+    static constexpr int q = 0, k = kTile, v = 2 * kTile, rec = 3 * kTile;
+    static constexpr int stage = (rec + Rec<DELTA>::bytes + 1023) / 1024 * 1024;
+    static constexpr int bar = kStages * stage;
+    static constexpr int bytes = bar + 256 + 1024;   // + room to align the base
+};
+
+// TMEM columns.  The bf16 pairs take one column per two values.
+constexpr uint32_t kTS = 0;        // S^T, FP32 [128 v][128 k]
+constexpr uint32_t kTSh = 128;     // S^T hi (64), lo (64)
+constexpr uint32_t kTU = 256;      // delta: (K S)^T, then U~^T, FP32 [128][64]; decay: V^T (32 columns)
+constexpr uint32_t kTO1 = 320;     // (Q S)^T
+constexpr uint32_t kTR = 384;      // delta: R^T hi, lo; decay: (diag(w) V)^T hi, lo
+constexpr uint32_t kTO2 = 448;     // (G R)^T or (P V)^T
+constexpr uint32_t kTUh = kTSh;    // delta: U~^T hi, lo: S's pair is used up by then
+
+// Barriers
+enum { kFull = 0, kEmpty = kStages, kBU0 = 2 * kStages, kBU, kBS, kCS, kCR, kCW, kCO, kDrain, kBars };
+
+template <bool DELTA>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    chain_kernel(const ChunkArgs ca, const __grid_constant__ CUtensorMap mq,
+                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using SM = ChainSmem<DELTA>;
+    using R = Rec<DELTA>;
+    const PrefillArgs& a = ca.p;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* sm = raw + (base - smem_u32(raw));
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int req = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int end = min(max(__ldg(a.cu_seqlens + req + 1), 0), a.max_tokens);
+    const int start = min(max(__ldg(a.cu_seqlens + req), 0), end);
+    const int len = end - start;
+    if (len == 0) return;
+    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)start * a.H + h) * D;
+    if (slot < 0 || slot >= a.n_slots) {
+        if (slot >= a.n_slots && tid == 0 && h == 0) atomicOr(a.status, DAMP_EFLAG_SLOT_RANGE);
+        for (long long e = tid; e < (long long)len * (D / 8); e += kChainThreads)
+            reinterpret_cast<uint4*>(out + (e / (D / 8)) * (size_t)a.H * D)[e % (D / 8)] =
+                make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int nc = (len + C - 1) / C;
+    // a plan's first_block + nc always fits; anything else is kept inside the workspace
+    const int fb = min(max(ca.first_block[req], 0), max(a.max_blocks - nc, 0));
+    const uint32_t bars = base + SM::bar;
+    auto bar = [&](int i) { return bars + 8 * i; };
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bar(kFull + i), 1);
+            mbar_init(bar(kEmpty + i), kComputeWarps);
+        }
+        mbar_init(bar(kBU0), 1);
+        mbar_init(bar(kBU), 1);
+        mbar_init(bar(kBS), 1);
+        mbar_init(bar(kCS), kComputeWarps);
+        mbar_init(bar(kCR), kComputeWarps);
+        mbar_init(bar(kCW), kComputeWarps);
+        mbar_init(bar(kCO), kComputeWarps);
+        mbar_init(bar(kDrain), 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == kComputeWarps) tmem_alloc(smem_u32(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    // Bounded wait; gives up at once where another warp gave up.
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar(i), parity)) return true;
+        const uint64_t began = global_ns();
+        for (uint32_t n = 1;; ++n) {
+            if (mbar_try_wait(bar(i), parity)) return true;
+            if (s_abort) return false;
+            if ((n & 63u) == 0 && global_ns() - began > a.wait_ns) {
+                s_abort = 1;
+                return false;
+            }
+        }
+    };
+
+    if (warp == kComputeWarps) {
+        // ---------------------------------------------------------- loader
+        if (lane == 0) {
+            const int hq = h / (a.H / a.H_qk);
+            int issued = 0;
+            for (int c = 0; c < nc; ++c) {
+                const int s = c % kStages;
+                if (c >= kStages && !wait(kEmpty + s, (c / kStages - 1) & 1)) break;
+                const uint32_t st = base + s * SM::stage, f = bar(kFull + s);
+                const int t = start + c * C;
+                mbar_arrive_expect_tx(f, 3 * kTile + R::bytes);
+                for (int half = 0; half < 2; ++half) {
+                    tma_load_3d(st + SM::k + half * kHalf, &mk, half * 64, hq, t, f);
+                    tma_load_3d(st + SM::v + half * kHalf, &mv, half * 64, h, t, f);
+                    tma_load_3d(st + SM::q + half * kHalf, &mq, half * 64, hq, t, f);
+                }
+                bulk_g2s(st + SM::rec, ca.records + ((size_t)(fb + c) * a.H + h) * R::bytes, R::bytes, f);
+                issued = c + 1;
+            }
+            // copies in flight end before the CTA does
+            for (int c = max(0, issued - kStages); c < issued; ++c)
+                mbar_wait_bounded(bar(kFull + c % kStages), (c / kStages) & 1, a.wait_ns);
+        }
+    } else if (warp == kComputeWarps + 1) {
+        // ---------------------------------------------------------- matrix instructions
+        if (lane == 0) {
+            constexpr uint32_t i64 = mma_idesc(128, 64, false, false);
+            constexpr uint32_t i128mn = mma_idesc(128, 128, false, true);
+            // D += A[tmem pair half] * B over K = 128 (B: 64 tokens x 128 channels)
+            auto over_channels = [&](uint32_t d, uint32_t at, uint32_t tile, bool first) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(tm + d, tm + at + 8 * ks,
+                           desc_k_major(tile + (ks >> 2) * kHalf + (ks & 3) * 32), i64,
+                           !(first && ks == 0));
+            };
+            // D += A * B over K = 64 tokens (B: C x C matrix of the record)
+            auto over_tokens = [&](uint32_t d, uint32_t at, uint32_t mat, bool first) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ts(tm + d, tm + at + 8 * ks, desc_k_major(mat + ks * 32), i64,
+                           !(first && ks == 0));
+            };
+            // S^T += A * K (B: 64 tokens x 128 channels, channels contiguous)
+            auto into_state = [&](uint32_t at, uint32_t tile) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ts(tm + kTS, tm + at + 8 * ks, desc_mn_major(tile + ks * 2048, kHalf), i128mn, 1);
+            };
+            bool ok = true;
+            for (int c = 0; c < nc && ok; ++c) {
+                const uint32_t st = base + (c % kStages) * SM::stage, rec = st + SM::rec;
+                const uint32_t ph = c & 1;
+                if (!(ok = wait(kFull + c % kStages, (c / kStages) & 1))) break;
+                if (!(ok = wait(kCS, ph))) break;
+                tc_fence_after();
+                if constexpr (DELTA) {
+                    over_channels(kTU, kTSh, st + SM::k, true);
+                    over_channels(kTU, kTSh + 64, st + SM::k, false);
+                    tc_commit(bar(kBU0));
+                }
+                if (c > 0 && !(ok = wait(kCO, ph ^ 1))) break;
+                tc_fence_after();
+                over_channels(kTO1, kTSh, st + SM::q, true);
+                over_channels(kTO1, kTSh + 64, st + SM::q, false);
+                if constexpr (DELTA) {
+                    if (!(ok = wait(kCR, ph))) break;
+                    tc_fence_after();
+                    over_tokens(kTU, kTR, rec + R::th, true);
+                    over_tokens(kTU, kTR + 32, rec + R::th, false);
+                    over_tokens(kTU, kTR, rec + R::tl, false);
+                    tc_commit(bar(kBU));
+                    over_tokens(kTO2, kTR, rec + R::gh, true);
+                    over_tokens(kTO2, kTR + 32, rec + R::gh, false);
+                    over_tokens(kTO2, kTR, rec + R::gl, false);
+                    if (!(ok = wait(kCW, ph))) break;
+                    tc_fence_after();
+                    into_state(kTUh, st + SM::k);
+                    into_state(kTUh + 32, st + SM::k);
+                } else {
+                    over_tokens(kTO2, kTU, rec + R::gh, true);
+                    over_tokens(kTO2, kTU, rec + R::gl, false);
+                    into_state(kTR, st + SM::k);
+                    into_state(kTR + 32, st + SM::k);
+                }
+                tc_commit(bar(kBS));
+            }
+            // nothing in flight when TMEM and shared memory are given back
+            tc_commit(bar(kDrain));
+            mbar_wait_bounded(bar(kDrain), 0, a.wait_ns);
+        }
+    } else {
+        // ---------------------------------------------------------- compute
+        const int quad = warp & 3, half = warp >> 2;       // TMEM lanes, column half
+        const uint32_t lanes = tm + ((uint32_t)(quad * 32) << 16);
+        const int vcol = quad * 32 + lane;                 // this thread's value column
+        auto arrive = [&](int i) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(i));
+        };
+        auto wait_all = [&](int i, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, wait(i, parity));
+        };
+        const size_t unit = (size_t)h * D * D * 4;
+        float* st_out = reinterpret_cast<float*>(
+            a.state + (size_t)(a.state_by_slot ? slot : req) * a.state_stride + unit);
+        const bool has = from >= 0 && from < a.n_slots;
+        const float* st_in = reinterpret_cast<const float*>(
+            a.state + (size_t)(a.state_by_slot ? (has ? from : slot) : req) * a.state_stride + unit);
+
+        // S^T columns [64 half, 64 half + 64) of the state, in two parts of 32
+        auto put_state = [&](int part, const uint32_t (&x)[32], float gc) {
+            uint32_t hi[16], lo[16], y[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                split_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), hi[i], lo[i]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(x[i]) * gc);
+            const uint32_t col = half * 64 + part * 32;
+            tmem_st16(lanes + kTSh + col / 2, hi);
+            tmem_st16(lanes + kTSh + 64 + col / 2, lo);
+            tmem_st32(lanes + kTS + col, y);
+        };
+        bool ok = true;
+        for (int c = 0; c <= nc; ++c) {
+            const uint32_t ph = c & 1;
+            uint8_t* st = sm + (c % kStages) * SM::stage;
+            uint8_t* rec = st + SM::rec;
+            const float* gam = reinterpret_cast<const float*>(rec + R::gam);
+            // ---- the state before block c
+            if (c > 0 && !(ok = wait_all(kBS, ph ^ 1))) break;
+            tc_fence_after();
+            if (c < nc && !(ok = wait_all(kFull + c % kStages, (c / kStages) & 1))) break;
+            const float gc = c < nc ? gam[C - 1] : 1.f;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint32_t x[32];
+                const int k0 = half * 64 + part * 32;
+                if (c == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = has ? __float_as_uint(st_in[(size_t)(k0 + i) * D + vcol]) : 0u;
+                } else {
+                    tmem_ld32(lanes + kTS + k0, x);
+                    tmem_wait_ld();
+                }
+                if (c < nc) {
+                    put_state(part, x, gc);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        st_out[(size_t)(k0 + i) * D + vcol] = __uint_as_float(x[i]);
+                }
+            }
+            const int live = min(C, len - c * C);         // tokens of block c
+            if (c < nc && live < C) {
+                // rows behind the request's end hold another request's keys: they
+                // must not enter the sums over tokens
+                for (int e = tid; e < (C - live) * 16; e += kComputeWarps * 32) {
+                    const int r = live + e / 16, u = e % 16;
+                    *reinterpret_cast<uint4*>(st + SM::k + (u >> 3) * kHalf + r * 128 + (u & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            // this thread's value column of V at token t
+            auto value = [&](int t) -> float {
+                const uint16_t b = *reinterpret_cast<const uint16_t*>(
+                    st + SM::v + (vcol >> 6) * kHalf + swz(t, (vcol & 63) * 2));
+                return t < live ? __uint_as_float((uint32_t)b << 16) : 0.f;
+            };
+            if (!DELTA && c < nc) {
+                const float* w = reinterpret_cast<const float*>(rec + R::w);
+                uint32_t vb[16], hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = half * 32 + 2 * i;
+                    const float x = value(t), y = value(t + 1);
+                    vb[i] = pack_bf16(x, y);               // exact: V is bf16
+                    split_bf16(w[t] * x, w[t + 1] * y, hi[i], lo[i]);
+                }
+                tmem_st16(lanes + kTU + half * 16, vb);
+                tmem_st16(lanes + kTR + half * 16, hi);
+                tmem_st16(lanes + kTR + 32 + half * 16, lo);
+            }
+            if (c < nc) {
+                tmem_wait_st();
+                arrive(kCS);
+            }
+            // ---- readout of block c - 1, behind the state on the chain
+            if (c > 0) {
+                const int p = c - 1;
+                const float* pg = reinterpret_cast<const float*>(
+                    sm + (p % kStages) * SM::stage + SM::rec + R::gam);
+                uint32_t o1[32], o2[32];
+                tmem_ld32(lanes + kTO1 + half * 32, o1);
+                tmem_ld32(lanes + kTO2 + half * 32, o2);
+                tmem_wait_ld();
+                float gt[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) gt[i] = pg[half * 32 + i];
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(kCO));
+                    mbar_arrive(bar(kEmpty + p % kStages));
+                }
+                const int first = p * C + half * 32;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (first + i < len)
+                        out[(size_t)(first + i) * a.H * D + vcol] = __float2bfloat16_rn(
+                            __fmaf_rn(gt[i], __uint_as_float(o1[i]), __uint_as_float(o2[i])));
+            }
+            if (c == nc) break;
+            if constexpr (DELTA) {
+                // ---- R = V - diag(gamma) K S
+                uint32_t x[32], hi[16], lo[16];
+                if (!(ok = wait_all(kBU0, ph))) break;
+                tc_fence_after();
+                tmem_ld32(lanes + kTU + half * 32, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = half * 32 + 2 * i;
+                    split_bf16(__fmaf_rn(-gam[t], __uint_as_float(x[2 * i]), value(t)),
+                               __fmaf_rn(-gam[t + 1], __uint_as_float(x[2 * i + 1]), value(t + 1)),
+                               hi[i], lo[i]);
+                }
+                tmem_st16(lanes + kTR + half * 16, hi);
+                tmem_st16(lanes + kTR + 32 + half * 16, lo);
+                tmem_wait_st();
+                arrive(kCR);
+                // ---- U~ as a pair
+                if (!(ok = wait_all(kBU, ph))) break;
+                tc_fence_after();
+                tmem_ld32(lanes + kTU + half * 32, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    split_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), hi[i], lo[i]);
+                tmem_st16(lanes + kTUh + half * 16, hi);
+                tmem_st16(lanes + kTUh + 32 + half * 16, lo);
+                tmem_wait_st();
+                arrive(kCW);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
+    if (warp == kComputeWarps) {
+        tc_fence_after();
+        tmem_free(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                 CUtensorMapFloatOOBfill);
+std::atomic<EncodeTiled> g_encode{nullptr};
+
+// Token rows of `heads` heads of 128 bf16 channels, in boxes of 64 rows of one
+// head's 64 channels, 128-byte swizzle; rows behind the last read as zeros.
+cudaError_t token_map(CUtensorMap* m, const void* p, int heads, long long rows, long long stride) {
+    EncodeTiled f = g_encode.load(std::memory_order_relaxed);
+    if (!f) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)C}, step[3] = {1, 1, 1};
+    const CUresult r = f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box,
+                         step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <bool DELTA>
+cudaError_t set_attributes() {
+    cudaError_t e = cudaFuncSetAttribute(prepare_kernel<DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PrepSmem<DELTA>::bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(chain_kernel<DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ChainSmem<DELTA>::bytes);
+}
+
+template <bool DELTA>
+cudaError_t launch_rule(const ChunkArgs& ca, const CUtensorMap& mq, const CUtensorMap& mk,
+                        const CUtensorMap& mv, cudaStream_t s) {
+    prepare_kernel<DELTA><<<dim3(ca.p.max_blocks, ca.p.H), kPrepThreads, PrepSmem<DELTA>::bytes, s>>>(ca);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    chain_kernel<DELTA><<<ca.p.n * ca.p.H, kChainThreads, ChainSmem<DELTA>::bytes, s>>>(ca, mq, mk, mv);
+    return cudaGetLastError();
+}
+
+size_t first_block_bytes(int n) { return ((size_t)n * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+cudaError_t prepare_prefill() {
+    if (!g_encode.load()) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess) return e != cudaSuccess ? e : cudaErrorNotSupported;
+        g_encode.store(reinterpret_cast<EncodeTiled>(f));
+    }
+    const cudaError_t e = set_attributes<true>();
+    return e != cudaSuccess ? e : set_attributes<false>();
+}
+
+bool prefill_chunk_fits(int d_k, int d_v, int bf16) { return bf16 && d_k == D && d_v == D; }
+
+size_t prefill_chunk_bytes(int n, int H, int max_blocks, int delta) {
+    return first_block_bytes(n) +
+           (size_t)max_blocks * H * (delta ? Rec<true>::bytes : Rec<false>::bytes);
+}
+
+cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
+    ChunkArgs ca{a, reinterpret_cast<int32_t*>(a.work), a.work + first_block_bytes(a.n)};
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = token_map(&mq, a.q, a.H_qk, a.max_tokens, a.q_stride);
+    if (e == cudaSuccess) e = token_map(&mk, a.k, a.H_qk, a.max_tokens, a.k_stride);
+    if (e == cudaSuccess) e = token_map(&mv, a.v, a.H, a.max_tokens, a.v_stride);
+    if (e != cudaSuccess) return e;
+    return a.delta ? launch_rule<true>(ca, mq, mk, mv, s) : launch_rule<false>(ca, mq, mk, mv, s);
+}
+
+}  // namespace damp
