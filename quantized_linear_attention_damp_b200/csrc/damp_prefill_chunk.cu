@@ -18,7 +18,10 @@
 //   chain (one CTA per request and head, blocks in order): the products with
 //     S, transposed so that the 128 value columns are the M dimension of every
 //     matrix instruction and S^T, R^T and U~^T = (T~ R)^T are A operands in
-//     TMEM.  S itself stays in TMEM in FP32 from the first block to the last.
+//     TMEM.  S itself stays in the compute warps' registers in FP32 from the
+//     first block to the last: a block's part comes out of TMEM and is added
+//     with one rounding (accumulating in TMEM over all blocks would let the
+//     tensor core's truncated sums drift).
 //
 // Precision: Q, K and V enter as the bf16 they are.  Every FP32 operand (S, R,
 // U~, T~, G, P) enters as a pair of bf16 values, hi + lo, which leaves 2^-17
@@ -387,7 +390,7 @@ struct ChainSmem {
 };
 
 // TMEM columns.  The bf16 pairs take one column per two values.
-constexpr uint32_t kTS = 0;        // S^T, FP32 [128 v][128 k]
+constexpr uint32_t kTS = 0;        // a block's part of S^T, FP32 [128 v][128 k]
 constexpr uint32_t kTSh = 128;     // S^T hi (64), lo (64)
 constexpr uint32_t kTU = 256;      // delta: (K S)^T, then U~^T, FP32 [128][64]; decay: V^T (32 columns)
 constexpr uint32_t kTO1 = 320;     // (Q S)^T
@@ -510,11 +513,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     mma_ts(tm + d, tm + at + 8 * ks, desc_k_major(mat + ks * 32), i64,
                            !(first && ks == 0));
             };
-            // S^T += A * K (B: 64 tokens x 128 channels, channels contiguous)
-            auto into_state = [&](uint32_t at, uint32_t tile) {
+            // the block's part of S^T: A * K (B: 64 tokens x 128 channels, channels contiguous)
+            auto into_state = [&](uint32_t at, uint32_t tile, bool first) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tm + kTS, tm + at + 8 * ks, desc_mn_major(tile + ks * 2048, kHalf), i128mn, 1);
+                    mma_ts(tm + kTS, tm + at + 8 * ks, desc_mn_major(tile + ks * 2048, kHalf), i128mn,
+                           !(first && ks == 0));
             };
             bool ok = true;
             for (int c = 0; c < nc && ok; ++c) {
@@ -544,13 +548,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     over_tokens(kTO2, kTR, rec + R::gl, false);
                     if (!(ok = wait(kCW, ph))) break;
                     tc_fence_after();
-                    into_state(kTUh, st + SM::k);
-                    into_state(kTUh + 32, st + SM::k);
+                    into_state(kTUh, st + SM::k, true);
+                    into_state(kTUh + 32, st + SM::k, false);
                 } else {
                     over_tokens(kTO2, kTU, rec + R::gh, true);
                     over_tokens(kTO2, kTU, rec + R::gl, false);
-                    into_state(kTR, st + SM::k);
-                    into_state(kTR + 32, st + SM::k);
+                    into_state(kTR, st + SM::k, true);
+                    into_state(kTR + 32, st + SM::k, false);
                 }
                 tc_commit(bar(kBS));
             }
@@ -578,19 +582,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const float* st_in = reinterpret_cast<const float*>(
             a.state + (size_t)(a.state_by_slot ? (has ? from : slot) : req) * a.state_stride + unit);
 
-        // S^T columns [64 half, 64 half + 64) of the state, in two parts of 32
-        auto put_state = [&](int part, const uint32_t (&x)[32], float gc) {
-            uint32_t hi[16], lo[16], y[32];
+        // this thread's part of the state: key rows [64 half, 64 half + 64) of its value column
+        float S[64];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                split_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), hi[i], lo[i]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(x[i]) * gc);
-            const uint32_t col = half * 64 + part * 32;
-            tmem_st16(lanes + kTSh + col / 2, hi);
-            tmem_st16(lanes + kTSh + 64 + col / 2, lo);
-            tmem_st32(lanes + kTS + col, y);
-        };
+        for (int i = 0; i < 64; ++i) S[i] = has ? st_in[(size_t)(half * 64 + i) * D + vcol] : 0.f;
         bool ok = true;
         for (int c = 0; c <= nc; ++c) {
             const uint32_t ph = c & 1;
@@ -601,25 +596,28 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             if (c > 0 && !(ok = wait_all(kBS, ph ^ 1))) break;
             tc_fence_after();
             if (c < nc && !(ok = wait_all(kFull + c % kStages, (c / kStages) & 1))) break;
-            const float gc = c < nc ? gam[C - 1] : 1.f;
+            if (c > 0) {
+                const float gc = reinterpret_cast<const float*>(
+                    sm + ((c - 1) % kStages) * SM::stage + SM::rec + R::gam)[C - 1];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                uint32_t x[32];
-                const int k0 = half * 64 + part * 32;
-                if (c == 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = has ? __float_as_uint(st_in[(size_t)(k0 + i) * D + vcol]) : 0u;
-                } else {
-                    tmem_ld32(lanes + kTS + k0, x);
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t x[32];
+                    tmem_ld32(lanes + kTS + half * 64 + part * 32, x);
                     tmem_wait_ld();
-                }
-                if (c < nc) {
-                    put_state(part, x, gc);
-                } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        st_out[(size_t)(k0 + i) * D + vcol] = __uint_as_float(x[i]);
+                        S[part * 32 + i] = __fmaf_rn(gc, S[part * 32 + i], __uint_as_float(x[i]));
+                }
+            }
+            if (c < nc) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        split_bf16(S[part * 32 + 2 * i], S[part * 32 + 2 * i + 1], hi[i], lo[i]);
+                    tmem_st16(lanes + kTSh + half * 32 + part * 16, hi);
+                    tmem_st16(lanes + kTSh + 64 + half * 32 + part * 16, lo);
                 }
             }
             const int live = min(C, len - c * C);         // tokens of block c
@@ -682,7 +680,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                         out[(size_t)(first + i) * a.H * D + vcol] = __float2bfloat16_rn(
                             __fmaf_rn(gt[i], __uint_as_float(o1[i]), __uint_as_float(o2[i])));
             }
-            if (c == nc) break;
+            if (c == nc) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) st_out[(size_t)(half * 64 + i) * D + vcol] = S[i];
+                break;
+            }
             if constexpr (DELTA) {
                 // ---- R = V - diag(gamma) K S
                 uint32_t x[32], hi[16], lo[16];
@@ -720,6 +722,718 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     __syncthreads();
     if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
     if (warp == kComputeWarps) {
+        tc_fence_after();
+        tmem_free(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------ delta: prepare
+//
+// 128 threads a (block, head), five CTAs an SM: the steps are short and each
+// waits for the one before, so it is the number of resident CTAs that keeps the
+// SM busy.  Q and K share their 34 KB with A and T (FP32) and then with the
+// finished record.
+
+// The record of one (block, head): C x C bf16 matrices with 128-byte rows
+// (K-major, 128-byte swizzle) in the order in which the chain's products take
+// them as one operand of 128 rows, then gamma_t and gamma_C / gamma_t.
+struct DRec {
+    static constexpr int th = 0, gh = kMat, tl = 2 * kMat, gl = 3 * kMat;   // T' hi, G hi, T' lo, G lo
+    static constexpr int gam = 4 * kMat, w = gam + 4 * C;
+    static constexpr int bytes = w + 4 * C;
+};
+
+constexpr int kFA = C + 4;             // floats of a row of A and T
+struct DPrep {
+    static constexpr int q = 0, k = C * kRowB;
+    static constexpr int a = 0, t = C * kFA * 4;       // over q and k
+    static constexpr int img = 0;                      // over a and t
+    static constexpr int dia = 2 * C * kRowB;          // Gamma of the diagonal 16 x 16 blocks [4][16][16]
+    static constexpr int vec = dia + 4 * 16 * 16 * 4;  // alpha, beta, pre, post, gamma, w
+    static constexpr int bytes = vec + 6 * C * 4 + 32;
+    static_assert(C * kFA * 4 <= C * kRowB, "A fits over Q, T over K");
+    static_assert(DRec::bytes <= 2 * C * kRowB, "the record fits over Q and K");
+};
+
+__global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(const ChunkArgs ca) {
+    const PrefillArgs& a = ca.p;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // heads of a block run side by side: their rows of Q and K are neighbours in memory
+    const int blk = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int4 row = __ldg(reinterpret_cast<const int4*>(a.block_table) + blk);
+    const int req = row.x, t0 = row.y, len = row.z;
+    if (req < 0 || req >= a.n || t0 < 0 || len < 1 || len > C || t0 > a.max_tokens - len) return;
+    if (h == 0 && row.w == 0 && tid == 0) ca.first_block[req] = blk;
+    const int slot = __ldg(a.store_slot + req);
+    if (slot < 0 || slot >= a.n_slots) return;
+    const int hq = h / (a.H / a.H_qk);
+    float* s_dia = reinterpret_cast<float*>(sm + DPrep::dia);
+    float* s_al = reinterpret_cast<float*>(sm + DPrep::vec);
+    float* s_be = s_al + C;
+    float* s_pre = s_al + 2 * C;     // product of alpha from the 16-token group's start to t
+    float* s_post = s_al + 3 * C;    // product of alpha behind s to its group's end
+    float* s_ga = s_al + 4 * C;
+    float* s_w = s_al + 5 * C;
+
+    // ---- Q and K rows (zeros behind the request's end), decays
+    {
+        const uint16_t* qg = static_cast<const uint16_t*>(a.q) + (size_t)t0 * a.q_stride + (size_t)hq * D;
+        const uint16_t* kg = static_cast<const uint16_t*>(a.k) + (size_t)t0 * a.k_stride + (size_t)hq * D;
+        const int r = tid >> 4, c = tid & 15;
+        uint4 kv[C / 8], qv[C / 8];
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            const int at = r + 8 * i;
+            kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
+            if (at < len) {
+                kv[i] = __ldg(reinterpret_cast<const uint4*>(kg + (size_t)at * a.k_stride) + c);
+                qv[i] = __ldg(reinterpret_cast<const uint4*>(qg + (size_t)at * a.q_stride) + c);
+            }
+        }
+        if (tid < C) {
+            s_al[tid] = tid < len ? __ldg(a.alpha + (size_t)(t0 + tid) * a.H + h) : 1.f;
+            s_be[tid] = tid < len ? __ldg(a.beta + (size_t)(t0 + tid) * a.H + h) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            *reinterpret_cast<uint4*>(sm + DPrep::k + (r + 8 * i) * kRowB + c * 16) = kv[i];
+            *reinterpret_cast<uint4*>(sm + DPrep::q + (r + 8 * i) * kRowB + c * 16) = qv[i];
+        }
+    }
+    __syncthreads();
+    // Gamma_ts inside a group of 16 tokens by running products down column s;
+    // between groups I > J it is pre_t * (whole groups between) * post_s
+    if (tid < C + 4) {
+        const int g0 = tid < C ? tid & ~15 : (tid - C) * 16, s = tid < C ? tid & 15 : -1;
+        float al[16], x = 1.f;
+#pragma unroll
+        for (int t = 0; t < 16; t += 4)
+            *reinterpret_cast<float4*>(al + t) = *reinterpret_cast<const float4*>(s_al + g0 + t);
+        float* to = tid < C ? s_dia + g0 * 16 + s : s_pre + g0;
+        const int step = tid < C ? 16 : 1;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            x = t > s ? x * al[t] : x;
+            if (t >= s) to[t * step] = x;
+        }
+        if (tid < C) s_post[tid] = x;
+    }
+
+    // ---- Q K^T and K K^T: warp w has rows [16 w, 16 w + 16), columns up to its diagonal
+    const uint32_t base = smem_u32(sm);
+    const int r0 = warp * 16, g = lane >> 2, c2 = (lane & 3) * 2;
+    float P[8][4], M[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) P[j][i] = M[j][i] = 0.f;
+    {
+        const uint32_t a_off = base + (r0 + (lane & 15)) * kRowB + (lane >> 4) * 16;
+        const uint32_t b_off = base + DPrep::k + ((lane & 7) + (lane >> 4) * 8) * kRowB + ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t qa[4], ka[4];
+            ldsm4(qa, a_off + DPrep::q + ks * 32);
+            ldsm4(ka, a_off + DPrep::k + ks * 32);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {      // two column tiles at a time
+                if (j > warp) break;
+                uint32_t b[4];
+                ldsm4(b, b_off + j * 16 * kRowB + ks * 32);
+                mma16816(P[2 * j], qa, b[0], b[1]);
+                mma16816(P[2 * j + 1], qa, b[2], b[3]);
+                mma16816(M[2 * j], ka, b[0], b[1]);
+                mma16816(M[2 * j + 1], ka, b[2], b[3]);
+            }
+        }
+    }
+    __syncthreads();                       // the decays are there; Q and K are used up
+
+    // ---- P = Q K^T o Gamma (registers), A = diag(beta) K K^T o Gamma below the diagonal (shared)
+    float* s_a = reinterpret_cast<float*>(sm + DPrep::a);
+    float* s_t = reinterpret_cast<float*>(sm + DPrep::t);
+    // whole-group products: all[J] = alpha over group J
+    const float all1 = s_pre[31], all2 = s_pre[47];
+#pragma unroll
+    for (int i2 = 0; i2 < 2; ++i2) {
+        const int t = r0 + g + 8 * i2;
+        const float be = s_be[t], pre = s_pre[t];
+        const bool row_live = t < len;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int J = j >> 1;
+            if (J > warp) break;           // above the diagonal: P stays zero, A is not read
+            // decay from the end of group J to the start of this warp's group
+            const float mid = J + 1 >= warp ? 1.f
+                              : (J == 0 ? (warp == 2 ? all1 : all1 * all2) : all2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int s = 8 * j + c2 + i;
+                float dec;
+                if (J == warp) dec = s <= t ? s_dia[t * 16 + (s & 15)] : 0.f;
+                else dec = pre * (mid * s_post[s]);
+                if (!row_live) dec = 0.f;
+                const float m = M[j][2 * i2 + i];
+                P[j][2 * i2 + i] = dec == 0.f ? 0.f : P[j][2 * i2 + i] * dec;
+                s_a[t * kFA + s] = s < t && dec != 0.f ? be * (m * dec) : 0.f;
+            }
+        }
+    }
+    if (tid < C) {
+        // gamma_t and gamma_C / gamma_t
+        const int I = tid >> 4;
+        const float all0 = s_pre[15], all3 = s_pre[63];
+        const float before = I == 0 ? 1.f : I == 1 ? all0 : I == 2 ? all0 * all1 : all0 * all1 * all2;
+        const float after = I == 3 ? 1.f : I == 2 ? all3 : I == 1 ? all2 * all3 : all1 * all2 * all3;
+        s_ga[tid] = before * s_pre[tid];
+        s_w[tid] = after * s_post[tid];
+    }
+    __syncthreads();
+    // ---- T = (I + A)^-1, lower triangle: the four 16 x 16 diagonal blocks by
+    // substitution (a lane a column), then pairs of blocks, then halves: the
+    // block below the diagonal is -T22 (A21 T11).  The unused upper blocks of
+    // T hold A21 T11.
+    if (lane < 16) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v0 = i == lane ? 1.f : 0.f, v1 = 0.f;
+            const float* ar = s_a + (r0 + i) * kFA + r0;
+#pragma unroll
+            for (int k = 0; k < i; k += 4) {
+                const float4 av = *reinterpret_cast<const float4*>(ar + k);
+                v0 = __fmaf_rn(-av.x, x[k], v0);
+                if (k + 1 < i) v1 = __fmaf_rn(-av.y, x[k + 1], v1);
+                if (k + 2 < i) v0 = __fmaf_rn(-av.z, x[k + 2], v0);
+                if (k + 3 < i) v1 = __fmaf_rn(-av.w, x[k + 3], v1);
+            }
+            x[i] = v0 + v1;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s_t[(r0 + i) * kFA + r0 + lane] = x[i];
+    }
+    __syncthreads();
+    {
+        // blocks (1, 0) and (3, 2), two warps each
+        const int m = (tid >> 6) * 32, i = (tid & 63) >> 2, j = (tid & 3) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto product = [&](const float* lhs, const float* rhs) {      // rows of 16, steps of 4
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const float4 av = *reinterpret_cast<const float4*>(lhs + k);
+                const float l[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const float4 tv = *reinterpret_cast<const float4*>(rhs + (k + kk) * kFA);
+                    r.x = __fmaf_rn(l[kk], tv.x, r.x);
+                    r.y = __fmaf_rn(l[kk], tv.y, r.y);
+                    r.z = __fmaf_rn(l[kk], tv.z, r.z);
+                    r.w = __fmaf_rn(l[kk], tv.w, r.w);
+                }
+            }
+            return r;
+        };
+        x = product(s_a + (m + 16 + i) * kFA + m, s_t + m * kFA + m + j);
+        *reinterpret_cast<float4*>(&s_t[(m + i) * kFA + m + 16 + j]) = x;
+        __syncthreads();
+        const float4 y = product(s_t + (m + 16 + i) * kFA + m + 16, s_t + m * kFA + m + 16 + j);
+        __syncthreads();
+        *reinterpret_cast<float4*>(&s_t[(m + 16 + i) * kFA + m + j]) = make_float4(-y.x, -y.y, -y.z, -y.w);
+        *reinterpret_cast<float4*>(&s_t[(m + i) * kFA + m + 16 + j]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    {
+        // the lower left 32 x 32 block: 2 rows x 4 columns a thread; a warp's
+        // columns (first product) or rows (second) bound the triangle it needs
+        float x[2][4] = {}, y[2][4] = {};
+        auto product = [&](float (&r)[2][4], const float* l0, const float* rhs, int k0, int k1) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                if (k < k0 || k >= k1) continue;      // the same for the whole warp
+                const float4 a0 = *reinterpret_cast<const float4*>(l0 + k);
+                const float4 a1 = *reinterpret_cast<const float4*>(l0 + kFA + k);
+                const float l[2][4] = {{a0.x, a0.y, a0.z, a0.w}, {a1.x, a1.y, a1.z, a1.w}};
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const float4 tv = *reinterpret_cast<const float4*>(rhs + (k + kk) * kFA);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        r[i][0] = __fmaf_rn(l[i][kk], tv.x, r[i][0]);
+                        r[i][1] = __fmaf_rn(l[i][kk], tv.y, r[i][1]);
+                        r[i][2] = __fmaf_rn(l[i][kk], tv.z, r[i][2]);
+                        r[i][3] = __fmaf_rn(l[i][kk], tv.w, r[i][3]);
+                    }
+                }
+            }
+        };
+        {
+            const int i = (lane >> 1) * 2, j = warp * 8 + (lane & 1) * 4;       // columns by warp
+            product(x, s_a + (32 + i) * kFA, s_t + j, warp * 8, 32);
+            *reinterpret_cast<float4*>(&s_t[i * kFA + 32 + j]) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+            *reinterpret_cast<float4*>(&s_t[(i + 1) * kFA + 32 + j]) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+        }
+        __syncthreads();
+        {
+            const int i = warp * 8 + (lane >> 3) * 2, j = (lane & 7) * 4;       // rows by warp
+            product(y, s_t + (32 + i) * kFA + 32, s_t + 32 + j, 0, warp * 8 + 8);
+            *reinterpret_cast<float4*>(&s_t[(32 + i) * kFA + j]) = make_float4(-y[0][0], -y[0][1], -y[0][2], -y[0][3]);
+            *reinterpret_cast<float4*>(&s_t[(33 + i) * kFA + j]) = make_float4(-y[1][0], -y[1][1], -y[1][2], -y[1][3]);
+        }
+    }
+    __syncthreads();
+    // ---- T' = T diag(beta) as bf16 pairs in the record's image (over A and T: through registers).
+    // Behind the request's end beta is zero, so those columns vanish, and A has no such rows.
+    uint8_t* img = sm + DPrep::img;
+    {
+        const int s = (tid & 15) * 4, r = tid >> 4;       // 4 columns, rows r, r + 8, ...
+        const float4 be = *reinterpret_cast<const float4*>(s_be + s);
+        uint2 hi[C / 8], lo[C / 8];
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            const int t = r + 8 * i;
+            const float4 tv = *reinterpret_cast<const float4*>(&s_t[t * kFA + s]);
+            split_bf16(s <= t ? tv.x * be.x : 0.f, s + 1 <= t ? tv.y * be.y : 0.f, hi[i].x, lo[i].x);
+            split_bf16(s + 2 <= t ? tv.z * be.z : 0.f, s + 3 <= t ? tv.w * be.w : 0.f, hi[i].y, lo[i].y);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            *reinterpret_cast<uint2*>(img + DRec::th + swz(r + 8 * i, s * 2)) = hi[i];
+            *reinterpret_cast<uint2*>(img + DRec::tl + swz(r + 8 * i, s * 2)) = lo[i];
+        }
+    }
+    if (tid < C) {
+        reinterpret_cast<float*>(img + DRec::gam)[tid] = s_ga[tid];
+        reinterpret_cast<float*>(img + DRec::w)[tid] = s_w[tid];
+    }
+    __syncthreads();
+    // ---- G = P T', over the k steps and column tiles the triangles leave
+    float (&G)[8][4] = M;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) G[j][i] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+        if (ks > warp) break;
+        uint32_t ph[4], pl[4];
+        split_bf16(P[2 * ks][0], P[2 * ks][1], ph[0], pl[0]);
+        split_bf16(P[2 * ks][2], P[2 * ks][3], ph[1], pl[1]);
+        split_bf16(P[2 * ks + 1][0], P[2 * ks + 1][1], ph[2], pl[2]);
+        split_bf16(P[2 * ks + 1][2], P[2 * ks + 1][3], ph[3], pl[3]);
+#pragma unroll
+        for (int j = 0; j <= ks; ++j) {
+            uint32_t bh[4], bl[4];
+            const uint32_t at = base + DPrep::img + swz(ks * 16 + (lane & 15), j * 32 + (lane >> 4) * 16);
+            ldsm4t(bh, at + DRec::th);
+            ldsm4t(bl, at + DRec::tl);
+            mma16816(G[2 * j], ph, bh[0], bh[1]);
+            mma16816(G[2 * j + 1], ph, bh[2], bh[3]);
+            mma16816(G[2 * j], pl, bh[0], bh[1]);
+            mma16816(G[2 * j + 1], pl, bh[2], bh[3]);
+            mma16816(G[2 * j], ph, bl[0], bl[1]);
+            mma16816(G[2 * j + 1], ph, bl[2], bl[3]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t hi, lo;
+            split_bf16(G[j][2 * i], G[j][2 * i + 1], hi, lo);
+            const uint32_t at = swz(r0 + g + 8 * i, (8 * j + c2) * 2);
+            *reinterpret_cast<uint32_t*>(img + DRec::gh + at) = hi;
+            *reinterpret_cast<uint32_t*>(img + DRec::gl + at) = lo;
+        }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+        bulk_s2g(ca.records + ((size_t)blk * a.H + h) * DRec::bytes, smem_u32(img), DRec::bytes);
+        bulk_commit();
+        bulk_wait_read<0>();
+    }
+}
+
+// ------------------------------------------------------------------ delta: chain
+
+// One CTA of 22 warps a (request, head): 16 keep the state and form the A
+// operands (warp w: TMEM lanes of w & 3, a quarter of the columns), 4 write the
+// readout, one loads, one issues the matrix instructions.
+//
+// What bounds it is the chain of one block after another: S as a pair -> K S ->
+// R as a pair -> U -> U as a pair -> the block's part of S -> S.  So Q S and
+// G R are products of their own behind the ones the chain waits for (K and Q
+// as one operand of 128 rows cost 1280 cycles against 768 + 768, but the chain
+// waits for all of them), and S's update and K S go by halves of the key
+// channels: one half's product runs while the other half's state is split.
+struct DChain {
+    static constexpr int kWarps = 16, kOut = 4;              // state warps, readout warps
+    static constexpr int threads = 32 * (kWarps + kOut + 2);
+    static constexpr int kq = 0, v = 2 * kTile, rec = 3 * kTile;   // K, Q by halves of 64 channels: K0 Q0 K1 Q1
+    static constexpr int stage = (rec + DRec::bytes + 1023) / 1024 * 1024;
+    static constexpr int out = kStages * stage;              // readout rows, 16 bytes apart in banks
+    static constexpr int out_row = D * 2 + 16;
+    static constexpr int bar = out + C * out_row;
+    static constexpr int bytes = bar + 256 + 1024;
+    // TMEM columns
+    static constexpr uint32_t dS = 0;       // the block's part of S^T, FP32 [128 v][128 k]
+    static constexpr uint32_t Sh = 128;     // S^T hi, lo (64 columns each)
+    static constexpr uint32_t Rh = 0;       // R^T hi, lo (32 each), while dS is not needed
+    static constexpr uint32_t Uh = 160;     // (diag(w) U)^T hi, over S's hi of the channels' second half,
+    static constexpr uint32_t Ul = 224;     // and lo over its lo: the first half's next pair is written
+                                            // while the second half's product still reads U
+    static constexpr uint32_t KQ = 256;     // (K S)^T, (Q S)^T, FP32 [128][64] each
+    static constexpr uint32_t UO = 384;     // U^T, (G R)^T
+    // Barriers.  B*: a product is done (KS; U; Q S and G R; S's two halves).  C*: the state
+    // warps have left an operand in TMEM (S's halves, R, U); CO: the readout is out of TMEM.
+    enum { Full = 0, Empty = kStages, BK = 2 * kStages, BU, BO, BS, CS = BS + 2, CR = CS + 2, CU, CO, Drain };
+};
+
+__global__ void __launch_bounds__(DChain::threads, 1)
+    delta_chain_kernel(const ChunkArgs ca, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using X = DChain;
+    const PrefillArgs& a = ca.p;
+    extern __shared__ __align__(1024) uint8_t sm_raw[];
+    const uint32_t base = (smem_u32(sm_raw) + 1023u) & ~1023u;
+    uint8_t* sm = sm_raw + (base - smem_u32(sm_raw));
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int req = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int end = min(max(__ldg(a.cu_seqlens + req + 1), 0), a.max_tokens);
+    const int start = min(max(__ldg(a.cu_seqlens + req), 0), end);
+    const int len = end - start;
+    if (len == 0) return;
+    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)start * a.H + h) * D;
+    if (slot < 0 || slot >= a.n_slots) {
+        if (slot >= a.n_slots && tid == 0 && h == 0) atomicOr(a.status, DAMP_EFLAG_SLOT_RANGE);
+        for (long long e = tid; e < (long long)len * (D / 8); e += X::threads)
+            reinterpret_cast<uint4*>(out + (e / (D / 8)) * (size_t)a.H * D)[e % (D / 8)] =
+                make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int nc = (len + C - 1) / C;
+    // a plan's first_block + nc always fits; anything else is kept inside the workspace
+    const int fb = min(max(ca.first_block[req], 0), max(a.max_blocks - nc, 0));
+    auto bar = [&](int i) { return base + X::bar + 8 * i; };
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bar(X::Full + i), 1);
+            mbar_init(bar(X::Empty + i), X::kWarps / 2 + X::kOut);
+        }
+        for (int i = X::BK; i < X::CS; ++i) mbar_init(bar(i), 1);
+        mbar_init(bar(X::CS), X::kWarps / 2);
+        mbar_init(bar(X::CS + 1), X::kWarps / 2);
+        mbar_init(bar(X::CR), X::kWarps);
+        mbar_init(bar(X::CU), X::kWarps);
+        mbar_init(bar(X::CO), X::kOut);
+        mbar_init(bar(X::Drain), 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == X::kWarps + X::kOut) tmem_alloc(smem_u32(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    // Bounded wait; gives up at once where another warp gave up.
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        // (the timer is slow to read: only a wait that lasts looks at it)
+        uint64_t began = 0;
+        for (uint32_t n = 1; !mbar_try_wait_short(bar(i), parity); ++n) {
+            // (the loader's waits are long and not on the chain: its polling would slow the
+            // others' shared memory)
+            if (warp == X::kWarps + X::kOut) __nanosleep(200);
+            if (n & 255u) continue;
+            if (s_abort) return false;
+            const uint64_t now = global_ns();
+            if (!began) began = now;
+            if (now - began > a.wait_ns) {
+                s_abort = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    auto wait_all = [&](int i, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(i, parity));
+    };
+    // A group of warps waits by one of them polling and the others at a hardware
+    // barrier: 20 polling warps would take the shared-memory pipe from the matrix
+    // instructions' operands.  All of the group get the same answer.
+    auto wait_group = [&](bool polls, int i, uint32_t parity, int id, int threads) -> bool {
+        const bool ok = !polls || wait_all(i, parity);
+        return !bar_red_or(id, threads, !ok);
+    };
+    auto arrive = [&](int i) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(i));
+    };
+    const int quad = warp & 3;
+    const uint32_t lanes = tm + ((uint32_t)(quad * 32) << 16);
+    const int vcol = quad * 32 + lane;                 // a state or readout thread's value column
+
+    if (warp < X::kWarps) {
+        // ---------------------------------------------------------- state
+        const int part = warp >> 2;                    // key channels [32 part, +32), tokens [16 part, +16)
+        const size_t unit = (size_t)h * D * D * 4;
+        const bool has = from >= 0 && from < a.n_slots;
+        float S[32];
+        {
+            const float* in = reinterpret_cast<const float*>(
+                a.state + (size_t)(a.state_by_slot ? (has ? from : slot) : req) * a.state_stride + unit);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = has ? in[(size_t)(part * 32 + i) * D + vcol] : 0.f;
+        }
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = c & 1;
+            uint8_t* st = sm + (c % kStages) * X::stage;
+            const float* gam = reinterpret_cast<const float*>(st + X::rec + DRec::gam);
+            const float* w = reinterpret_cast<const float*>(st + X::rec + DRec::w);
+            // ---- the state before block c as a pair
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) split_bf16(S[2 * i], S[2 * i + 1], hi[i], lo[i]);
+            tmem_st16(lanes + X::Sh + part * 16, hi);
+            tmem_st16(lanes + X::Sh + 64 + part * 16, lo);
+            const int live = min(C, len - c * C);         // tokens of block c
+            if (live < C) {
+                // rows behind the request's end hold another request's keys and values:
+                // they must not enter the sums over tokens
+                if (!(ok = wait_group(quad + (part & 1) == 0, X::Full + c % kStages, (c / kStages) & 1,
+                                      2 + part / 2, X::kWarps * 16)))
+                    break;
+                // (a half of the channels by the warps that hand over that half)
+                for (int e = tid % (X::kWarps * 16); e < (C - live) * 8; e += X::kWarps * 16) {
+                    const int at = (live + e / 8) * 128 + (e % 8) * 16;
+                    *reinterpret_cast<uint4*>(st + X::kq + part / 2 * kTile + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(st + X::v + part / 2 * kHalf + at) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            arrive(X::CS + part / 2);
+            //@CK(1)
+            // ---- R = V - diag(gamma) K S
+            if (!(ok = wait_group(warp == 0, X::Full + c % kStages, (c / kStages) & 1, 4, X::kWarps * 32)))
+                break;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int t = part * 16 + i;
+                const uint16_t b = *reinterpret_cast<const uint16_t*>(
+                    st + X::v + (vcol >> 6) * kHalf + swz(t, (vcol & 63) * 2));
+                v[i] = __uint_as_float((uint32_t)b << 16);
+            }
+            uint32_t x[16], h8[8], l8[8];
+            if (!(ok = wait_group(warp == 0, X::BK, ph, 4, X::kWarps * 32))) break;
+            //@CK(2)
+            tc_fence_after();
+            tmem_ld16(lanes + X::KQ + part * 16, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                split_bf16(__fmaf_rn(-gam[part * 16 + 2 * i], __uint_as_float(x[2 * i]), v[2 * i]),
+                           __fmaf_rn(-gam[part * 16 + 2 * i + 1], __uint_as_float(x[2 * i + 1]), v[2 * i + 1]),
+                           h8[i], l8[i]);
+            tmem_st8(lanes + X::Rh + part * 8, h8);
+            tmem_st8(lanes + X::Rh + 32 + part * 8, l8);
+            tmem_wait_st();
+            arrive(X::CR);
+            //@CK(3)
+            // ---- diag(w) U as a pair
+            if (!(ok = wait_group(warp == 0, X::BU, ph, 4, X::kWarps * 32))) break;
+            //@CK(4)
+            tc_fence_after();
+            tmem_ld16(lanes + X::UO + part * 16, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                split_bf16(w[part * 16 + 2 * i] * __uint_as_float(x[2 * i]),
+                           w[part * 16 + 2 * i + 1] * __uint_as_float(x[2 * i + 1]), h8[i], l8[i]);
+            tmem_st8(lanes + X::Uh + part * 8, h8);
+            tmem_st8(lanes + X::Ul + part * 8, l8);
+            const float gc = gam[C - 1];
+            tmem_wait_st();
+            arrive(X::CU);
+            //@CK(5)
+            // ---- S <- gamma_C S + the block's part
+            if (!(ok = wait_group(quad + (part & 1) == 0, X::BS + part / 2, ph, 2 + part / 2, X::kWarps * 16)))
+                break;
+            //@CK(6)
+            tc_fence_after();
+            uint32_t y[32];
+            tmem_ld32(lanes + X::dS + part * 32, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = __fmaf_rn(gc, S[i], __uint_as_float(y[i]));
+            // The stage is used up: the second half's product was its last reader, and
+            // every state warp had its values out before that product was issued.
+            if (part >= 2 && lane == 0) mbar_arrive(bar(X::Empty + c % kStages));
+        }
+        if (ok) {
+            float* to = reinterpret_cast<float*>(
+                a.state + (size_t)(a.state_by_slot ? slot : req) * a.state_stride + unit);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) to[(size_t)(part * 32 + i) * D + vcol] = S[i];
+        }
+    } else if (warp < X::kWarps + X::kOut) {
+        // ---------------------------------------------------------- readout
+        const int wt = tid - X::kWarps * 32;
+        uint8_t* so = sm + X::out;
+        for (int c = 0; c < nc; ++c) {
+            const float* gam = reinterpret_cast<const float*>(sm + (c % kStages) * X::stage + X::rec + DRec::gam);
+            if (!wait_group(warp == X::kWarps, X::BO, c & 1, 1, X::kOut * 32)) break;
+            tc_fence_after();
+            // out of TMEM first: the next block's Q S waits for that
+            uint32_t o[C / 2];
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                uint32_t o1[16], o2[16];
+                tmem_ld16(lanes + X::KQ + 64 + part * 16, o1);
+                tmem_ld16(lanes + X::UO + 64 + part * 16, o2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 gt = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
+                    o[part * 8 + i] = pack_bf16(
+                        __fmaf_rn(gt.x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
+                        __fmaf_rn(gt.y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
+                }
+            }
+            arrive(X::CO);
+            if (lane == 0) mbar_arrive(bar(X::Empty + c % kStages));
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) {
+                *reinterpret_cast<uint16_t*>(so + 2 * i * X::out_row + vcol * 2) = (uint16_t)o[i];
+                *reinterpret_cast<uint16_t*>(so + (2 * i + 1) * X::out_row + vcol * 2) = (uint16_t)(o[i] >> 16);
+            }
+            bar_sync(1, X::kOut * 32);
+            const int live = min(C, len - c * C);
+#pragma unroll
+            for (int i = 0; i < C * 16 / (X::kOut * 32); ++i) {
+                const int r = (wt >> 4) + i * (X::kOut * 2), u = wt & 15;
+                if (r < live)
+                    *reinterpret_cast<uint4*>(out + (size_t)(c * C + r) * a.H * D + u * 8) =
+                        *reinterpret_cast<const uint4*>(so + r * X::out_row + u * 16);
+            }
+            bar_sync(1, X::kOut * 32);
+        }
+    } else if (warp == X::kWarps + X::kOut) {
+        // ---------------------------------------------------------- loads
+        const int hq = h / (a.H / a.H_qk);
+        int issued = 0;
+        for (int c = 0; c < nc; ++c) {
+            const int s = c % kStages;
+            if (c >= kStages && !wait_all(X::Empty + s, (c / kStages - 1) & 1)) break;
+            const uint32_t st = base + s * X::stage, f = bar(X::Full + s);
+            const int t = start + c * C;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(f, 3 * kTile + DRec::bytes);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    tma_load_3d(st + X::kq + half * kTile, &mk, half * 64, hq, t, f);
+                    tma_load_3d(st + X::kq + half * kTile + kHalf, &mq, half * 64, hq, t, f);
+                    tma_load_3d(st + X::v + half * kHalf, &mv, half * 64, h, t, f);
+                }
+                bulk_g2s(st + X::rec, ca.records + ((size_t)(fb + c) * a.H + h) * DRec::bytes,
+                         DRec::bytes, f);
+                // a stage is not free early enough to cover DRAM's latency: the next blocks come
+                // to L2 ahead of their turn
+                for (int n = c == 0 ? 1 : kStages; n <= kStages && c + n < nc; ++n) {
+                    const int tn = t + n * C;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        tma_prefetch_3d(&mk, half * 64, hq, tn);
+                        tma_prefetch_3d(&mq, half * 64, hq, tn);
+                        tma_prefetch_3d(&mv, half * 64, h, tn);
+                    }
+                    bulk_prefetch(ca.records + ((size_t)(fb + c + n) * a.H + h) * DRec::bytes, DRec::bytes);
+                }
+            }
+            issued = c + 1;
+        }
+        // copies in flight end before the CTA does
+        for (int c = max(0, issued - kStages); c < issued; ++c)
+            mbar_wait_bounded(bar(X::Full + c % kStages), (c / kStages) & 1, a.wait_ns);
+    } else {
+        // ---------------------------------------------------------- matrix instructions
+        // One at a time in order; what the state warps wait for goes first, the
+        // readout's products run while they work on its result.
+        constexpr uint32_t idk = mma_idesc(128, 64, false, false), idmn = mma_idesc(128, 64, false, true);
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t st = base + (c % kStages) * X::stage, rec = st + X::rec;
+            const uint32_t ph = c & 1;
+            if (!wait_all(X::Full + c % kStages, (c / kStages) & 1)) break;
+            if (c > 0 && !wait_all(X::CO, ph ^ 1)) break;
+            // (K S)^T, the channels' first half as soon as it is there; each hi, then lo
+            bool ok = true;
+#pragma unroll
+            for (int half = 0; half < 2 && ok; ++half) {
+                if (!(ok = wait_all(X::CS + half, ph))) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tm + X::KQ, tm + X::Sh + (ks >> 2) * 64 + half * 32 + (ks & 3) * 8,
+                               desc_k_major(st + X::kq + half * kTile + (ks & 3) * 32), idk, half + ks > 0);
+                    if (half == 1) {
+                        tc_commit(bar(X::BK));
+                        // (Q S)^T, while the state warps work on R
+#pragma unroll
+                        for (int ks = 0; ks < 16; ++ks)
+                            mma_ts(tm + X::KQ + 64, tm + X::Sh + 8 * ks,
+                                   desc_k_major(st + X::kq + ((ks >> 2) & 1) * kTile + kHalf + (ks & 3) * 32),
+                                   idk, ks > 0);
+                    }
+                }
+            }
+            if (!ok) break;
+            // U^T = (T' R)^T, then (G R)^T: hi * hi, lo * hi, hi * lo
+            if (!wait_all(X::CR, ph)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 12; ++ks)
+                    mma_ts(tm + X::UO, tm + X::Rh + 8 * (ks & 7),
+                           desc_k_major(rec + (ks < 8 ? DRec::th : DRec::tl) + (ks & 3) * 32), idk, ks > 0);
+                tc_commit(bar(X::BU));
+#pragma unroll
+                for (int ks = 0; ks < 12; ++ks)
+                    mma_ts(tm + X::UO + 64, tm + X::Rh + 8 * (ks & 7),
+                           desc_k_major(rec + (ks < 8 ? DRec::gh : DRec::gl) + (ks & 3) * 32), idk, ks > 0);
+                tc_commit(bar(X::BO));
+            }
+            // the block's part of S^T, by halves of its channels
+            if (!wait_all(X::CU, ph)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tm + X::dS + half * 64, tm + (ks < 4 ? X::Uh : X::Ul) + 8 * (ks & 3),
+                               desc_mn_major(st + X::kq + half * kTile + (ks & 3) * 2048, kTile), idmn, ks > 0);
+                    tc_commit(bar(X::BS + half));
+                }
+            }
+        }
+        // nothing in flight when TMEM and shared memory are given back
+        if (elect_one()) tc_commit(bar(X::Drain));
+        mbar_wait_bounded(bar(X::Drain), 0, a.wait_ns);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
+    if (warp == X::kWarps + X::kOut) {
         tc_fence_after();
         tmem_free(tm, 512);
     }
@@ -778,7 +1492,11 @@ cudaError_t prepare_prefill() {
         if (e != cudaSuccess || q != cudaDriverEntryPointSuccess) return e != cudaSuccess ? e : cudaErrorNotSupported;
         g_encode.store(reinterpret_cast<EncodeTiled>(f));
     }
-    const cudaError_t e = set_attributes<true>();
+    cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         DPrep::bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 DChain::bytes);
     return e != cudaSuccess ? e : set_attributes<false>();
 }
 
@@ -786,7 +1504,7 @@ bool prefill_chunk_fits(int d_k, int d_v, int bf16) { return bf16 && d_k == D &&
 
 size_t prefill_chunk_bytes(int n, int H, int max_blocks, int delta) {
     return first_block_bytes(n) +
-           (size_t)max_blocks * H * (delta ? Rec<true>::bytes : Rec<false>::bytes);
+           (size_t)max_blocks * H * (delta ? DRec::bytes : Rec<false>::bytes);
 }
 
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
@@ -796,7 +1514,11 @@ cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = token_map(&mk, a.k, a.H_qk, a.max_tokens, a.k_stride);
     if (e == cudaSuccess) e = token_map(&mv, a.v, a.H, a.max_tokens, a.v_stride);
     if (e != cudaSuccess) return e;
-    return a.delta ? launch_rule<true>(ca, mq, mk, mv, s) : launch_rule<false>(ca, mq, mk, mv, s);
+    if (!a.delta) return launch_rule<false>(ca, mq, mk, mv, s);
+    delta_prepare_kernel<<<a.max_blocks * a.H, kPrepThreads, DPrep::bytes, s>>>(ca);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    delta_chain_kernel<<<a.n * a.H, DChain::threads, DChain::bytes, s>>>(ca, mq, mk, mv);
+    return cudaGetLastError();
 }
 
 }  // namespace damp
