@@ -553,7 +553,7 @@ int prefill_space(const damp_pool* pool, int rule, int n, int max_tokens, int in
     w->chunked = damp::prefill_chunk_fits(d.d_k, d.d_v, in_dtype == DAMP_DTYPE_BF16);
     int blocks = 0;
     damp_plan_blocks(n, max_tokens, &blocks);
-    w->total = w->states + (w->chunked ? damp::prefill_chunk_bytes(n, d.H, blocks,
+    w->total = w->states + (w->chunked ? damp::prefill_chunk_bytes(n, d.H, max_tokens, blocks,
                                                                    rule == DAMP_RULE_DELTA)
                                        : 0);
     return DAMP_OK;

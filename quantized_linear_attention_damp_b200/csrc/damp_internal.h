@@ -175,7 +175,7 @@ cudaError_t launch_prefill_tokens(const PrefillArgs& a, cudaStream_t stream);
 // (damp_pool_create calls it, outside any stream capture).
 cudaError_t prepare_prefill();
 bool prefill_chunk_fits(int d_k, int d_v, int bf16);
-size_t prefill_chunk_bytes(int n, int H, int max_blocks, int delta);
+size_t prefill_chunk_bytes(int n, int H, int max_tokens, int max_blocks, int delta);
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t stream);
 
 // Launchers (damp_decode.cu, damp_codec.cu, damp_calib.cu).  They return cudaError_t.

@@ -43,20 +43,10 @@ namespace {
 
 constexpr int C = DAMP_PLAN_BLOCK;     // tokens of a block
 constexpr int D = 128;                 // d_k = d_v
+constexpr int kSms = 148;              // of a B200: how work is cut, not how it is launched
 static_assert(C == 64, "the kernels' tiles are 64 tokens");
 
-// What the prepare kernel leaves for one (block, head), as the shared-memory
-// image the chain kernel copies: C x C bf16 matrices with 128-byte rows
-// (K-major, 128-byte swizzle), then gamma_t and gamma_C / gamma_t as FP32.
 constexpr int kMat = C * C * 2;                                  // 8192
-template <bool DELTA>
-struct Rec {
-    static constexpr int th = 0, tl = kMat;                      // T~ hi, lo (delta)
-    static constexpr int gh = DELTA ? 2 * kMat : 0, gl = gh + kMat;   // G (or P) hi, lo
-    static constexpr int gam = gl + kMat, w = gam + 4 * C;
-    static constexpr int bytes = w + 4 * C;
-};
-
 __device__ __forceinline__ uint32_t swz(int row, int byte) {     // byte in 0..127 of a 128-byte row
     return (uint32_t)(row * 128 + (byte ^ ((row & 7) << 4)));
 }
@@ -90,641 +80,29 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 constexpr int kPrepThreads = 128;
 constexpr int kRowB = (D + 8) * 2;     // bytes of a staged Q or K row (8 extra values: no bank conflicts)
-constexpr int kF = C + 8;              // floats of a row of the FP32 matrices
-constexpr int kTB = (C + 8) * 2;       // bytes of a row of the bf16 T'
 
-template <bool DELTA>
-struct PrepSmem {
-    static constexpr int k = 0, q = C * kRowB;
-    static constexpr int img = 0;                                  // over k and q, once they are used up
-    static constexpr int dec = 2 * C * kRowB;                      // Gamma, FP32 [C][kF]
-    static constexpr int tb = dec;                                 // T' hi, lo (bf16), over Gamma
-    static constexpr int a = dec + C * kF * 4;                     // A, FP32
-    static constexpr int t = a + (DELTA ? C * kF * 4 : 0);         // (I + A)^-1, FP32
-    static constexpr int vec = t + (DELTA ? C * kF * 4 : 0);       // alpha, beta, gamma, w
-    static constexpr int bytes = vec + 4 * C * 4;
-    static_assert(Rec<DELTA>::bytes <= 2 * C * kRowB, "image fits over k and q");
-    static_assert(2 * C * kTB <= C * kF * 4, "T' fits over Gamma");
-};
-
-template <bool DELTA>
-__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const ChunkArgs ca) {
-    using S = PrepSmem<DELTA>;
-    using R = Rec<DELTA>;
-    const PrefillArgs& a = ca.p;
-    extern __shared__ __align__(1024) uint8_t sm[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int blk = blockIdx.x, h = blockIdx.y;
-    const int4 row = __ldg(reinterpret_cast<const int4*>(a.block_table) + blk);
-    const int req = row.x, t0 = row.y, len = row.z;
-    if (req < 0 || req >= a.n || t0 < 0 || len < 1 || len > C || t0 > a.max_tokens - len) return;
-    if (h == 0 && row.w == 0 && tid == 0) ca.first_block[req] = blk;
-    const int slot = __ldg(a.store_slot + req);
-    if (slot < 0 || slot >= a.n_slots) return;
-    const int hq = h / (a.H / a.H_qk);
-    float* s_dec = reinterpret_cast<float*>(sm + S::dec);
-    float* s_al = reinterpret_cast<float*>(sm + S::vec);
-    float* s_be = s_al + C;
-    float* s_ga = s_al + 2 * C;
-    float* s_w = s_al + 3 * C;
-
-    // ---- Q and K rows (zeros behind the request's end), decays
-    const uint16_t* qg = static_cast<const uint16_t*>(a.q) + (size_t)t0 * a.q_stride + (size_t)hq * D;
-    const uint16_t* kg = static_cast<const uint16_t*>(a.k) + (size_t)t0 * a.k_stride + (size_t)hq * D;
-#pragma unroll
-    for (int i = 0; i < C * (D / 8) / kPrepThreads; ++i) {
-        const int e = tid + i * kPrepThreads, r = e / (D / 8), c = e % (D / 8);
-        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
-        if (r < len) {
-            kv = __ldg(reinterpret_cast<const uint4*>(kg + (size_t)r * a.k_stride) + c);
-            qv = __ldg(reinterpret_cast<const uint4*>(qg + (size_t)r * a.q_stride) + c);
-        }
-        *reinterpret_cast<uint4*>(sm + S::k + r * kRowB + c * 16) = kv;
-        *reinterpret_cast<uint4*>(sm + S::q + r * kRowB + c * 16) = qv;
-    }
-    if (tid < C) {
-        s_al[tid] = tid < len ? __ldg(a.alpha + (size_t)(t0 + tid) * a.H + h) : 1.f;
-        if (DELTA) s_be[tid] = tid < len ? __ldg(a.beta + (size_t)(t0 + tid) * a.H + h) : 0.f;
-    }
-    __syncthreads();
-    // thread s: Gamma_ts down column s; thread C: gamma_t
-    if (tid < C) {
-        float x = 1.f;
-        s_dec[tid * kF + tid] = 1.f;
-        for (int t = tid + 1; t < C; ++t) {
-            x *= s_al[t];
-            s_dec[t * kF + tid] = x;
-        }
-        s_w[tid] = x;
-    } else if (tid == C) {
-        float x = 1.f;
-        for (int t = 0; t < C; ++t) {
-            x *= s_al[t];
-            s_ga[t] = x;
-        }
-    }
-
-    // ---- Q K^T and K K^T: warp w has rows [16 w, 16 w + 16), columns up to its diagonal
-    const uint32_t base = smem_u32(sm);
-    const int r0 = warp * 16, g = lane >> 2, c2 = (lane & 3) * 2;
-    float P[8][4], M[8][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) P[j][i] = M[j][i] = 0.f;
-    const uint32_t a_off = (r0 + (lane & 15)) * kRowB + (lane >> 4) * 16;
-    const uint32_t b_off = ((lane & 7) + (lane >> 4) * 8) * kRowB + ((lane >> 3) & 1) * 16;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t qa[4], ka[4];
-        ldsm4(qa, base + S::q + a_off + ks * 32);
-        if (DELTA) ldsm4(ka, base + S::k + a_off + ks * 32);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {      // two column tiles at a time
-            if (j > warp) break;
-            uint32_t b[4];
-            ldsm4(b, base + S::k + j * 16 * kRowB + b_off + ks * 32);
-            mma16816(P[2 * j], qa, b[0], b[1]);
-            mma16816(P[2 * j + 1], qa, b[2], b[3]);
-            if (DELTA) {
-                mma16816(M[2 * j], ka, b[0], b[1]);
-                mma16816(M[2 * j + 1], ka, b[2], b[3]);
-            }
-        }
-    }
-    __syncthreads();                       // Gamma is there; Q and K are used up
-
-    // ---- P = Q K^T o Gamma, A = diag(beta) K K^T o Gamma below the diagonal
-    float* s_a = reinterpret_cast<float*>(sm + S::a);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = r0 + g + (i >> 1) * 8, s = 8 * j + c2 + (i & 1);
-            const bool seen = s <= t && t < len;
-            const float dec = seen ? s_dec[t * kF + s] : 0.f;
-            P[j][i] = seen ? P[j][i] * dec : 0.f;
-            if (DELTA) s_a[t * kF + s] = s < t && t < len ? s_be[t] * (M[j][i] * dec) : 0.f;
-        }
-
-    uint8_t* img = sm + S::img;
-    if constexpr (DELTA) {
-        float* s_t = reinterpret_cast<float*>(sm + S::t);
-        __syncthreads();
-        // ---- (I + A)^-1, lower triangle: the four 16 x 16 diagonal blocks by
-        // substitution (lane = column), then pairs of blocks, then halves:
-        // the block below the diagonal is -T22 (A21 T11).  The unused upper
-        // blocks hold A21 T11.
-        if (lane < 16) {
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float v = i == lane ? 1.f : 0.f;
-                const float* ar = s_a + (r0 + i) * kF + r0;
-#pragma unroll
-                for (int k = 0; k < i; ++k) v = __fmaf_rn(-ar[k], x[k], v);
-                x[i] = v;
-                s_t[(r0 + i) * kF + r0 + lane] = v;
-            }
-        }
-        __syncthreads();
-        {
-            const int m = (tid >> 6) * 32, i = (tid & 63) >> 2, j = (tid & 3) * 4;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float av = s_a[(m + 16 + i) * kF + m + k];
-                const float4 tv = *reinterpret_cast<const float4*>(&s_t[(m + k) * kF + m + j]);
-                x[0] = __fmaf_rn(av, tv.x, x[0]);
-                x[1] = __fmaf_rn(av, tv.y, x[1]);
-                x[2] = __fmaf_rn(av, tv.z, x[2]);
-                x[3] = __fmaf_rn(av, tv.w, x[3]);
-            }
-            *reinterpret_cast<float4*>(&s_t[(m + i) * kF + m + 16 + j]) =
-                make_float4(x[0], x[1], x[2], x[3]);
-            __syncthreads();
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float av = -s_t[(m + 16 + i) * kF + m + 16 + k];
-                const float4 tv = *reinterpret_cast<const float4*>(&s_t[(m + k) * kF + m + 16 + j]);
-                y[0] = __fmaf_rn(av, tv.x, y[0]);
-                y[1] = __fmaf_rn(av, tv.y, y[1]);
-                y[2] = __fmaf_rn(av, tv.z, y[2]);
-                y[3] = __fmaf_rn(av, tv.w, y[3]);
-            }
-            *reinterpret_cast<float4*>(&s_t[(m + 16 + i) * kF + m + j]) =
-                make_float4(y[0], y[1], y[2], y[3]);
-            __syncthreads();
-            // the scratch above the diagonal is zero for the next level
-            *reinterpret_cast<float4*>(&s_t[(m + i) * kF + m + 16 + j]) =
-                make_float4(0.f, 0.f, 0.f, 0.f);
-            // (and the diagonal blocks' own upper triangles are zeros of the substitution)
-            __syncthreads();
-        }
-        {
-            const int i = tid >> 2, j = (tid & 3) * 8;
-            float x[8] = {};
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float av = s_a[(32 + i) * kF + k];
-                const float4 t1 = *reinterpret_cast<const float4*>(&s_t[k * kF + j]);
-                const float4 t2 = *reinterpret_cast<const float4*>(&s_t[k * kF + j + 4]);
-                x[0] = __fmaf_rn(av, t1.x, x[0]);
-                x[1] = __fmaf_rn(av, t1.y, x[1]);
-                x[2] = __fmaf_rn(av, t1.z, x[2]);
-                x[3] = __fmaf_rn(av, t1.w, x[3]);
-                x[4] = __fmaf_rn(av, t2.x, x[4]);
-                x[5] = __fmaf_rn(av, t2.y, x[5]);
-                x[6] = __fmaf_rn(av, t2.z, x[6]);
-                x[7] = __fmaf_rn(av, t2.w, x[7]);
-            }
-            *reinterpret_cast<float4*>(&s_t[i * kF + 32 + j]) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(&s_t[i * kF + 36 + j]) = make_float4(x[4], x[5], x[6], x[7]);
-            __syncthreads();
-            float y[8] = {};
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float av = -s_t[(32 + i) * kF + 32 + k];
-                const float4 t1 = *reinterpret_cast<const float4*>(&s_t[k * kF + 32 + j]);
-                const float4 t2 = *reinterpret_cast<const float4*>(&s_t[k * kF + 36 + j]);
-                y[0] = __fmaf_rn(av, t1.x, y[0]);
-                y[1] = __fmaf_rn(av, t1.y, y[1]);
-                y[2] = __fmaf_rn(av, t1.z, y[2]);
-                y[3] = __fmaf_rn(av, t1.w, y[3]);
-                y[4] = __fmaf_rn(av, t2.x, y[4]);
-                y[5] = __fmaf_rn(av, t2.y, y[5]);
-                y[6] = __fmaf_rn(av, t2.z, y[6]);
-                y[7] = __fmaf_rn(av, t2.w, y[7]);
-            }
-            *reinterpret_cast<float4*>(&s_t[(32 + i) * kF + j]) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4*>(&s_t[(32 + i) * kF + 4 + j]) = make_float4(y[4], y[5], y[6], y[7]);
-            __syncthreads();
-        }
-        // ---- T' = T diag(beta) as bf16 pairs for the product below, and T~ = diag(w) T' into the
-        // image.  Rows behind the end: beta is zero, so their columns vanish; their rows may not
-        // (nothing reads U there, but K's rows are zero as well).
-        for (int e = tid; e < C * C / 2; e += kPrepThreads) {
-            const int t = e / (C / 2), s = e % (C / 2) * 2;
-            const float2 tv = *reinterpret_cast<const float2*>(&s_t[t * kF + s]);
-            const float x = s <= t ? tv.x * s_be[s] : 0.f, y = s + 1 <= t ? tv.y * s_be[s + 1] : 0.f;
-            uint32_t hi, lo;
-            split_bf16(x, y, hi, lo);
-            *reinterpret_cast<uint32_t*>(sm + S::tb + t * kTB + s * 2) = hi;
-            *reinterpret_cast<uint32_t*>(sm + S::tb + C * kTB + t * kTB + s * 2) = lo;
-            split_bf16(s_w[t] * x, s_w[t] * y, hi, lo);
-            *reinterpret_cast<uint32_t*>(img + R::th + swz(t, s * 2)) = hi;
-            *reinterpret_cast<uint32_t*>(img + R::tl + swz(t, s * 2)) = lo;
-        }
-        __syncthreads();
-        // ---- G = P T', over the k steps and column tiles the triangles leave
-        float G[8][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) G[j][i] = 0.f;
-        const uint32_t t_off = base + S::tb + (lane & 15) * kTB + (lane >> 4) * 16;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            if (ks > warp) break;
-            uint32_t ph[4], pl[4];
-            split_bf16(P[2 * ks][0], P[2 * ks][1], ph[0], pl[0]);
-            split_bf16(P[2 * ks][2], P[2 * ks][3], ph[1], pl[1]);
-            split_bf16(P[2 * ks + 1][0], P[2 * ks + 1][1], ph[2], pl[2]);
-            split_bf16(P[2 * ks + 1][2], P[2 * ks + 1][3], ph[3], pl[3]);
-#pragma unroll
-            for (int j = 0; j <= ks; ++j) {
-                uint32_t bh[4], bl[4];
-                ldsm4t(bh, t_off + ks * 16 * kTB + j * 32);
-                ldsm4t(bl, t_off + C * kTB + ks * 16 * kTB + j * 32);
-                mma16816(G[2 * j], ph, bh[0], bh[1]);
-                mma16816(G[2 * j + 1], ph, bh[2], bh[3]);
-                mma16816(G[2 * j], pl, bh[0], bh[1]);
-                mma16816(G[2 * j + 1], pl, bh[2], bh[3]);
-                mma16816(G[2 * j], ph, bl[0], bl[1]);
-                mma16816(G[2 * j + 1], ph, bl[2], bl[3]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) P[j][i] = G[j][i];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t hi, lo;
-            split_bf16(P[j][2 * i], P[j][2 * i + 1], hi, lo);
-            const uint32_t at = swz(r0 + g + 8 * i, (8 * j + c2) * 2);
-            *reinterpret_cast<uint32_t*>(img + R::gh + at) = hi;
-            *reinterpret_cast<uint32_t*>(img + R::gl + at) = lo;
-        }
-    if (tid < C) {
-        reinterpret_cast<float*>(img + R::gam)[tid] = s_ga[tid];
-        reinterpret_cast<float*>(img + R::w)[tid] = s_w[tid];
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-        bulk_s2g(ca.records + ((size_t)blk * a.H + h) * R::bytes, smem_u32(img), R::bytes);
-        bulk_commit();
-        bulk_wait_all<0>();
-    }
-}
-
-// ------------------------------------------------------------------ chain
-
-constexpr int kChainThreads = 320;     // 8 compute warps, the loader, the issuer of matrix instructions
-constexpr int kComputeWarps = 8;
-constexpr int kStages = 2;
 constexpr int kTile = C * D * 2;       // bytes of a Q, K or V tile: two halves of 64 channels
 constexpr int kHalf = kTile / 2;
 
-template <bool DELTA>
-struct ChainSmem {
-    static constexpr int q = 0, k = kTile, v = 2 * kTile, rec = 3 * kTile;
-    static constexpr int stage = (rec + Rec<DELTA>::bytes + 1023) / 1024 * 1024;
-    static constexpr int bar = kStages * stage;
-    static constexpr int bytes = bar + 256 + 1024;   // + room to align the base
-};
-
-// TMEM columns.  The bf16 pairs take one column per two values.
-constexpr uint32_t kTS = 0;        // a block's part of S^T, FP32 [128 v][128 k]
-constexpr uint32_t kTSh = 128;     // S^T hi (64), lo (64)
-constexpr uint32_t kTU = 256;      // delta: (K S)^T, then U~^T, FP32 [128][64]; decay: V^T (32 columns)
-constexpr uint32_t kTO1 = 320;     // (Q S)^T
-constexpr uint32_t kTR = 384;      // delta: R^T hi, lo; decay: (diag(w) V)^T hi, lo
-constexpr uint32_t kTO2 = 448;     // (G R)^T or (P V)^T
-constexpr uint32_t kTUh = kTSh;    // delta: U~^T hi, lo: S's pair is used up by then
-
-// Barriers
-enum { kFull = 0, kEmpty = kStages, kBU0 = 2 * kStages, kBU, kBS, kCS, kCR, kCW, kCO, kDrain, kBars };
-
-template <bool DELTA>
-__global__ void __launch_bounds__(kChainThreads, 1)
-    chain_kernel(const ChunkArgs ca, const __grid_constant__ CUtensorMap mq,
-                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-    using SM = ChainSmem<DELTA>;
-    using R = Rec<DELTA>;
-    const PrefillArgs& a = ca.p;
-    extern __shared__ uint8_t raw[];
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    uint8_t* sm = raw + (base - smem_u32(raw));
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int req = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const int end = min(max(__ldg(a.cu_seqlens + req + 1), 0), a.max_tokens);
-    const int start = min(max(__ldg(a.cu_seqlens + req), 0), end);
-    const int len = end - start;
-    if (len == 0) return;
-    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)start * a.H + h) * D;
-    if (slot < 0 || slot >= a.n_slots) {
-        if (slot >= a.n_slots && tid == 0 && h == 0) atomicOr(a.status, DAMP_EFLAG_SLOT_RANGE);
-        for (long long e = tid; e < (long long)len * (D / 8); e += kChainThreads)
-            reinterpret_cast<uint4*>(out + (e / (D / 8)) * (size_t)a.H * D)[e % (D / 8)] =
-                make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const int nc = (len + C - 1) / C;
-    // a plan's first_block + nc always fits; anything else is kept inside the workspace
-    const int fb = min(max(ca.first_block[req], 0), max(a.max_blocks - nc, 0));
-    const uint32_t bars = base + SM::bar;
-    auto bar = [&](int i) { return bars + 8 * i; };
-
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(bar(kFull + i), 1);
-            mbar_init(bar(kEmpty + i), kComputeWarps);
-        }
-        mbar_init(bar(kBU0), 1);
-        mbar_init(bar(kBU), 1);
-        mbar_init(bar(kBS), 1);
-        mbar_init(bar(kCS), kComputeWarps);
-        mbar_init(bar(kCR), kComputeWarps);
-        mbar_init(bar(kCW), kComputeWarps);
-        mbar_init(bar(kCO), kComputeWarps);
-        mbar_init(bar(kDrain), 1);
-        fence_mbar_init();
-        s_abort = 0;
-    }
-    if (warp == kComputeWarps) tmem_alloc(smem_u32(&s_tmem), 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = s_tmem;
-
-    // Bounded wait; gives up at once where another warp gave up.
-    auto wait = [&](int i, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar(i), parity)) return true;
-        const uint64_t began = global_ns();
-        for (uint32_t n = 1;; ++n) {
-            if (mbar_try_wait(bar(i), parity)) return true;
-            if (s_abort) return false;
-            if ((n & 63u) == 0 && global_ns() - began > a.wait_ns) {
-                s_abort = 1;
-                return false;
-            }
-        }
-    };
-
-    if (warp == kComputeWarps) {
-        // ---------------------------------------------------------- loader
-        if (lane == 0) {
-            const int hq = h / (a.H / a.H_qk);
-            int issued = 0;
-            for (int c = 0; c < nc; ++c) {
-                const int s = c % kStages;
-                if (c >= kStages && !wait(kEmpty + s, (c / kStages - 1) & 1)) break;
-                const uint32_t st = base + s * SM::stage, f = bar(kFull + s);
-                const int t = start + c * C;
-                mbar_arrive_expect_tx(f, 3 * kTile + R::bytes);
-                for (int half = 0; half < 2; ++half) {
-                    tma_load_3d(st + SM::k + half * kHalf, &mk, half * 64, hq, t, f);
-                    tma_load_3d(st + SM::v + half * kHalf, &mv, half * 64, h, t, f);
-                    tma_load_3d(st + SM::q + half * kHalf, &mq, half * 64, hq, t, f);
-                }
-                bulk_g2s(st + SM::rec, ca.records + ((size_t)(fb + c) * a.H + h) * R::bytes, R::bytes, f);
-                issued = c + 1;
-            }
-            // copies in flight end before the CTA does
-            for (int c = max(0, issued - kStages); c < issued; ++c)
-                mbar_wait_bounded(bar(kFull + c % kStages), (c / kStages) & 1, a.wait_ns);
-        }
-    } else if (warp == kComputeWarps + 1) {
-        // ---------------------------------------------------------- matrix instructions
-        if (lane == 0) {
-            constexpr uint32_t i64 = mma_idesc(128, 64, false, false);
-            constexpr uint32_t i128mn = mma_idesc(128, 128, false, true);
-            // D += A[tmem pair half] * B over K = 128 (B: 64 tokens x 128 channels)
-            auto over_channels = [&](uint32_t d, uint32_t at, uint32_t tile, bool first) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(tm + d, tm + at + 8 * ks,
-                           desc_k_major(tile + (ks >> 2) * kHalf + (ks & 3) * 32), i64,
-                           !(first && ks == 0));
-            };
-            // D += A * B over K = 64 tokens (B: C x C matrix of the record)
-            auto over_tokens = [&](uint32_t d, uint32_t at, uint32_t mat, bool first) {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tm + d, tm + at + 8 * ks, desc_k_major(mat + ks * 32), i64,
-                           !(first && ks == 0));
-            };
-            // the block's part of S^T: A * K (B: 64 tokens x 128 channels, channels contiguous)
-            auto into_state = [&](uint32_t at, uint32_t tile, bool first) {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tm + kTS, tm + at + 8 * ks, desc_mn_major(tile + ks * 2048, kHalf), i128mn,
-                           !(first && ks == 0));
-            };
-            bool ok = true;
-            for (int c = 0; c < nc && ok; ++c) {
-                const uint32_t st = base + (c % kStages) * SM::stage, rec = st + SM::rec;
-                const uint32_t ph = c & 1;
-                if (!(ok = wait(kFull + c % kStages, (c / kStages) & 1))) break;
-                if (!(ok = wait(kCS, ph))) break;
-                tc_fence_after();
-                if constexpr (DELTA) {
-                    over_channels(kTU, kTSh, st + SM::k, true);
-                    over_channels(kTU, kTSh + 64, st + SM::k, false);
-                    tc_commit(bar(kBU0));
-                }
-                if (c > 0 && !(ok = wait(kCO, ph ^ 1))) break;
-                tc_fence_after();
-                over_channels(kTO1, kTSh, st + SM::q, true);
-                over_channels(kTO1, kTSh + 64, st + SM::q, false);
-                if constexpr (DELTA) {
-                    if (!(ok = wait(kCR, ph))) break;
-                    tc_fence_after();
-                    over_tokens(kTU, kTR, rec + R::th, true);
-                    over_tokens(kTU, kTR + 32, rec + R::th, false);
-                    over_tokens(kTU, kTR, rec + R::tl, false);
-                    tc_commit(bar(kBU));
-                    over_tokens(kTO2, kTR, rec + R::gh, true);
-                    over_tokens(kTO2, kTR + 32, rec + R::gh, false);
-                    over_tokens(kTO2, kTR, rec + R::gl, false);
-                    if (!(ok = wait(kCW, ph))) break;
-                    tc_fence_after();
-                    into_state(kTUh, st + SM::k, true);
-                    into_state(kTUh + 32, st + SM::k, false);
-                } else {
-                    over_tokens(kTO2, kTU, rec + R::gh, true);
-                    over_tokens(kTO2, kTU, rec + R::gl, false);
-                    into_state(kTR, st + SM::k, true);
-                    into_state(kTR + 32, st + SM::k, false);
-                }
-                tc_commit(bar(kBS));
-            }
-            // nothing in flight when TMEM and shared memory are given back
-            tc_commit(bar(kDrain));
-            mbar_wait_bounded(bar(kDrain), 0, a.wait_ns);
-        }
-    } else {
-        // ---------------------------------------------------------- compute
-        const int quad = warp & 3, half = warp >> 2;       // TMEM lanes, column half
-        const uint32_t lanes = tm + ((uint32_t)(quad * 32) << 16);
-        const int vcol = quad * 32 + lane;                 // this thread's value column
-        auto arrive = [&](int i) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(i));
-        };
-        auto wait_all = [&](int i, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, wait(i, parity));
-        };
-        const size_t unit = (size_t)h * D * D * 4;
-        float* st_out = reinterpret_cast<float*>(
-            a.state + (size_t)(a.state_by_slot ? slot : req) * a.state_stride + unit);
-        const bool has = from >= 0 && from < a.n_slots;
-        const float* st_in = reinterpret_cast<const float*>(
-            a.state + (size_t)(a.state_by_slot ? (has ? from : slot) : req) * a.state_stride + unit);
-
-        // this thread's part of the state: key rows [64 half, 64 half + 64) of its value column
-        float S[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = has ? st_in[(size_t)(half * 64 + i) * D + vcol] : 0.f;
-        bool ok = true;
-        for (int c = 0; c <= nc; ++c) {
-            const uint32_t ph = c & 1;
-            uint8_t* st = sm + (c % kStages) * SM::stage;
-            uint8_t* rec = st + SM::rec;
-            const float* gam = reinterpret_cast<const float*>(rec + R::gam);
-            // ---- the state before block c
-            if (c > 0 && !(ok = wait_all(kBS, ph ^ 1))) break;
-            tc_fence_after();
-            if (c < nc && !(ok = wait_all(kFull + c % kStages, (c / kStages) & 1))) break;
-            if (c > 0) {
-                const float gc = reinterpret_cast<const float*>(
-                    sm + ((c - 1) % kStages) * SM::stage + SM::rec + R::gam)[C - 1];
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t x[32];
-                    tmem_ld32(lanes + kTS + half * 64 + part * 32, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        S[part * 32 + i] = __fmaf_rn(gc, S[part * 32 + i], __uint_as_float(x[i]));
-                }
-            }
-            if (c < nc) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        split_bf16(S[part * 32 + 2 * i], S[part * 32 + 2 * i + 1], hi[i], lo[i]);
-                    tmem_st16(lanes + kTSh + half * 32 + part * 16, hi);
-                    tmem_st16(lanes + kTSh + 64 + half * 32 + part * 16, lo);
-                }
-            }
-            const int live = min(C, len - c * C);         // tokens of block c
-            if (c < nc && live < C) {
-                // rows behind the request's end hold another request's keys: they
-                // must not enter the sums over tokens
-                for (int e = tid; e < (C - live) * 16; e += kComputeWarps * 32) {
-                    const int r = live + e / 16, u = e % 16;
-                    *reinterpret_cast<uint4*>(st + SM::k + (u >> 3) * kHalf + r * 128 + (u & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-            }
-            // this thread's value column of V at token t
-            auto value = [&](int t) -> float {
-                const uint16_t b = *reinterpret_cast<const uint16_t*>(
-                    st + SM::v + (vcol >> 6) * kHalf + swz(t, (vcol & 63) * 2));
-                return t < live ? __uint_as_float((uint32_t)b << 16) : 0.f;
-            };
-            if (!DELTA && c < nc) {
-                const float* w = reinterpret_cast<const float*>(rec + R::w);
-                uint32_t vb[16], hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = half * 32 + 2 * i;
-                    const float x = value(t), y = value(t + 1);
-                    vb[i] = pack_bf16(x, y);               // exact: V is bf16
-                    split_bf16(w[t] * x, w[t + 1] * y, hi[i], lo[i]);
-                }
-                tmem_st16(lanes + kTU + half * 16, vb);
-                tmem_st16(lanes + kTR + half * 16, hi);
-                tmem_st16(lanes + kTR + 32 + half * 16, lo);
-            }
-            if (c < nc) {
-                tmem_wait_st();
-                arrive(kCS);
-            }
-            // ---- readout of block c - 1, behind the state on the chain
-            if (c > 0) {
-                const int p = c - 1;
-                const float* pg = reinterpret_cast<const float*>(
-                    sm + (p % kStages) * SM::stage + SM::rec + R::gam);
-                uint32_t o1[32], o2[32];
-                tmem_ld32(lanes + kTO1 + half * 32, o1);
-                tmem_ld32(lanes + kTO2 + half * 32, o2);
-                tmem_wait_ld();
-                float gt[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) gt[i] = pg[half * 32 + i];
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(kCO));
-                    mbar_arrive(bar(kEmpty + p % kStages));
-                }
-                const int first = p * C + half * 32;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (first + i < len)
-                        out[(size_t)(first + i) * a.H * D + vcol] = __float2bfloat16_rn(
-                            __fmaf_rn(gt[i], __uint_as_float(o1[i]), __uint_as_float(o2[i])));
-            }
-            if (c == nc) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) st_out[(size_t)(half * 64 + i) * D + vcol] = S[i];
-                break;
-            }
-            if constexpr (DELTA) {
-                // ---- R = V - diag(gamma) K S
-                uint32_t x[32], hi[16], lo[16];
-                if (!(ok = wait_all(kBU0, ph))) break;
-                tc_fence_after();
-                tmem_ld32(lanes + kTU + half * 32, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = half * 32 + 2 * i;
-                    split_bf16(__fmaf_rn(-gam[t], __uint_as_float(x[2 * i]), value(t)),
-                               __fmaf_rn(-gam[t + 1], __uint_as_float(x[2 * i + 1]), value(t + 1)),
-                               hi[i], lo[i]);
-                }
-                tmem_st16(lanes + kTR + half * 16, hi);
-                tmem_st16(lanes + kTR + 32 + half * 16, lo);
-                tmem_wait_st();
-                arrive(kCR);
-                // ---- U~ as a pair
-                if (!(ok = wait_all(kBU, ph))) break;
-                tc_fence_after();
-                tmem_ld32(lanes + kTU + half * 32, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    split_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), hi[i], lo[i]);
-                tmem_st16(lanes + kTUh + half * 16, hi);
-                tmem_st16(lanes + kTUh + 32 + half * 16, lo);
-                tmem_wait_st();
-                arrive(kCW);
-            }
+// Waits for a phase of an mbarrier, at most wait_ns; gives up at once where
+// another warp gave up.  A patient waiter (the loader, whose waits are long
+// and not on the chain) sleeps between its looks: polling takes shared-memory
+// bandwidth from everyone else.
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint64_t wait_ns,
+                                             volatile int* abort, bool patient) {
+    uint64_t began = 0;
+    for (uint32_t n = 1; !mbar_try_wait_short(bar, parity); ++n) {
+        if (patient) __nanosleep(200);
+        if (n & 255u) continue;                // (the timer is slow to read)
+        if (*abort) return false;
+        const uint64_t now = global_ns();
+        if (!began) began = now;
+        if (now - began > wait_ns) {
+            *abort = 1;
+            return false;
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
-    if (warp == kComputeWarps) {
-        tc_fence_after();
-        tmem_free(tm, 512);
-    }
+    return true;
 }
 
 // ------------------------------------------------------------------ delta: prepare
@@ -758,11 +136,14 @@ struct DPrep {
 __global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(const ChunkArgs ca) {
     const PrefillArgs& a = ca.p;
     extern __shared__ __align__(1024) uint8_t sm[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     // heads of a block run side by side: their rows of Q and K are neighbours in memory
     const int blk = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int4 row = __ldg(reinterpret_cast<const int4*>(a.block_table) + blk);
     const int req = row.x, t0 = row.y, len = row.z;
+    // the triangles give the later row groups more work: a different warp has them in each CTA,
+    // or one scheduler of the SM would do most of it
+    const int warp = ((tid >> 5) + blk + h) & 3;
     if (req < 0 || req >= a.n || t0 < 0 || len < 1 || len > C || t0 > a.max_tokens - len) return;
     if (h == 0 && row.w == 0 && tid == 0) ca.first_block[req] = blk;
     const int slot = __ldg(a.store_slot + req);
@@ -1070,6 +451,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(const Ch
 // channels: one half's product runs while the other half's state is split.
 struct DChain {
     static constexpr int kWarps = 16, kOut = 4;              // state warps, readout warps
+    static constexpr int kStages = 2;
     static constexpr int threads = 32 * (kWarps + kOut + 2);
     static constexpr int kq = 0, v = 2 * kTile, rec = 3 * kTile;   // K, Q by halves of 64 channels: K0 Q0 K1 Q1
     static constexpr int stage = (rec + DRec::bytes + 1023) / 1024 * 1024;
@@ -1122,7 +504,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     auto bar = [&](int i) { return base + X::bar + 8 * i; };
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < X::kStages; ++i) {
             mbar_init(bar(X::Full + i), 1);
             mbar_init(bar(X::Empty + i), X::kWarps / 2 + X::kOut);
         }
@@ -1142,27 +524,9 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     tc_fence_after();
     const uint32_t tm = s_tmem;
 
-    // Bounded wait; gives up at once where another warp gave up.
-    auto wait = [&](int i, uint32_t parity) -> bool {
-        // (the timer is slow to read: only a wait that lasts looks at it)
-        uint64_t began = 0;
-        for (uint32_t n = 1; !mbar_try_wait_short(bar(i), parity); ++n) {
-            // (the loader's waits are long and not on the chain: its polling would slow the
-            // others' shared memory)
-            if (warp == X::kWarps + X::kOut) __nanosleep(200);
-            if (n & 255u) continue;
-            if (s_abort) return false;
-            const uint64_t now = global_ns();
-            if (!began) began = now;
-            if (now - began > a.wait_ns) {
-                s_abort = 1;
-                return false;
-            }
-        }
-        return true;
-    };
     auto wait_all = [&](int i, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait(i, parity));
+        return __all_sync(0xffffffffu, bounded_wait(bar(i), parity, a.wait_ns, &s_abort,
+                                                    warp == X::kWarps + X::kOut));
     };
     // A group of warps waits by one of them polling and the others at a hardware
     // barrier: 20 polling warps would take the shared-memory pipe from the matrix
@@ -1195,7 +559,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
         bool ok = true;
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
-            uint8_t* st = sm + (c % kStages) * X::stage;
+            uint8_t* st = sm + (c % X::kStages) * X::stage;
             const float* gam = reinterpret_cast<const float*>(st + X::rec + DRec::gam);
             const float* w = reinterpret_cast<const float*>(st + X::rec + DRec::w);
             // ---- the state before block c as a pair
@@ -1208,7 +572,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             if (live < C) {
                 // rows behind the request's end hold another request's keys and values:
                 // they must not enter the sums over tokens
-                if (!(ok = wait_group(quad + (part & 1) == 0, X::Full + c % kStages, (c / kStages) & 1,
+                if (!(ok = wait_group(quad + (part & 1) == 0, X::Full + c % X::kStages, (c / X::kStages) & 1,
                                       2 + part / 2, X::kWarps * 16)))
                     break;
                 // (a half of the channels by the warps that hand over that half)
@@ -1223,7 +587,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             arrive(X::CS + part / 2);
             //@CK(1)
             // ---- R = V - diag(gamma) K S
-            if (!(ok = wait_group(warp == 0, X::Full + c % kStages, (c / kStages) & 1, 4, X::kWarps * 32)))
+            if (!(ok = wait_group(warp == 0, X::Full + c % X::kStages, (c / X::kStages) & 1, 4, X::kWarps * 32)))
                 break;
             float v[16];
 #pragma unroll
@@ -1277,7 +641,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             for (int i = 0; i < 32; ++i) S[i] = __fmaf_rn(gc, S[i], __uint_as_float(y[i]));
             // The stage is used up: the second half's product was its last reader, and
             // every state warp had its values out before that product was issued.
-            if (part >= 2 && lane == 0) mbar_arrive(bar(X::Empty + c % kStages));
+            if (part >= 2 && lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
         }
         if (ok) {
             float* to = reinterpret_cast<float*>(
@@ -1290,7 +654,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
         const int wt = tid - X::kWarps * 32;
         uint8_t* so = sm + X::out;
         for (int c = 0; c < nc; ++c) {
-            const float* gam = reinterpret_cast<const float*>(sm + (c % kStages) * X::stage + X::rec + DRec::gam);
+            const float* gam = reinterpret_cast<const float*>(sm + (c % X::kStages) * X::stage + X::rec + DRec::gam);
             if (!wait_group(warp == X::kWarps, X::BO, c & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             // out of TMEM first: the next block's Q S waits for that
@@ -1310,7 +674,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                 }
             }
             arrive(X::CO);
-            if (lane == 0) mbar_arrive(bar(X::Empty + c % kStages));
+            if (lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) {
                 *reinterpret_cast<uint16_t*>(so + 2 * i * X::out_row + vcol * 2) = (uint16_t)o[i];
@@ -1332,8 +696,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
         const int hq = h / (a.H / a.H_qk);
         int issued = 0;
         for (int c = 0; c < nc; ++c) {
-            const int s = c % kStages;
-            if (c >= kStages && !wait_all(X::Empty + s, (c / kStages - 1) & 1)) break;
+            const int s = c % X::kStages;
+            if (c >= X::kStages && !wait_all(X::Empty + s, (c / X::kStages - 1) & 1)) break;
             const uint32_t st = base + s * X::stage, f = bar(X::Full + s);
             const int t = start + c * C;
             if (elect_one()) {
@@ -1348,7 +712,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                          DRec::bytes, f);
                 // a stage is not free early enough to cover DRAM's latency: the next blocks come
                 // to L2 ahead of their turn
-                for (int n = c == 0 ? 1 : kStages; n <= kStages && c + n < nc; ++n) {
+                for (int n = c == 0 ? 1 : X::kStages; n <= X::kStages && c + n < nc; ++n) {
                     const int tn = t + n * C;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -1362,17 +726,17 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             issued = c + 1;
         }
         // copies in flight end before the CTA does
-        for (int c = max(0, issued - kStages); c < issued; ++c)
-            mbar_wait_bounded(bar(X::Full + c % kStages), (c / kStages) & 1, a.wait_ns);
+        for (int c = max(0, issued - X::kStages); c < issued; ++c)
+            mbar_wait_bounded(bar(X::Full + c % X::kStages), (c / X::kStages) & 1, a.wait_ns);
     } else {
         // ---------------------------------------------------------- matrix instructions
         // One at a time in order; what the state warps wait for goes first, the
         // readout's products run while they work on its result.
         constexpr uint32_t idk = mma_idesc(128, 64, false, false), idmn = mma_idesc(128, 64, false, true);
         for (int c = 0; c < nc; ++c) {
-            const uint32_t st = base + (c % kStages) * X::stage, rec = st + X::rec;
+            const uint32_t st = base + (c % X::kStages) * X::stage, rec = st + X::rec;
             const uint32_t ph = c & 1;
-            if (!wait_all(X::Full + c % kStages, (c / kStages) & 1)) break;
+            if (!wait_all(X::Full + c % X::kStages, (c / X::kStages) & 1)) break;
             if (c > 0 && !wait_all(X::CO, ph ^ 1)) break;
             // (K S)^T, the channels' first half as soon as it is there; each hi, then lo
             bool ok = true;
@@ -1439,6 +803,466 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     }
 }
 
+// ------------------------------------------------------------------ decay
+
+// One CTA of 26 warps a (request, head, segment): 16 keep the state, 4 form
+// diag(w) V and P = Q K^T o Gamma, 4 write the readout, one loads (and
+// multiplies the decays up), one issues the matrix instructions.  Without the
+// delta rule a block's part of S does not depend on S, so operands are formed
+// ahead and the tensor core always has a product to work on (cycles a block):
+//   dS = (diag(w) V)^T K   A pair in TMEM                                    640
+//   S^T Q^T                A pair in TMEM                                    768
+//   Q K^T                  of the next block, as two products of 32 columns
+//                          whose tokens lie in lanes 0..63 and 64..127: all
+//                          four warps (and schedulers) share what follows   1024
+//   V^T P^T                A from V's tile as it is, B pair in shared memory 640
+// (Q K^T by mma.sync, in the warps that form the operands, took 2800.)
+// A request's blocks may be cut into segments that run side by side (few
+// chains would leave SMs idle): a first pass (SUM) leaves each segment's sum
+// and decay, and the segments of the second start from what those add up to.
+struct EChain {
+    static constexpr int kWarps = 16, kForm = 4, kOut = 4;
+    static constexpr int wOut = kWarps + kForm, wLoad = wOut + kOut, wMma = wLoad + 1;
+    static constexpr int threads = 32 * (wMma + 1);
+    static constexpr int kStages = 3;
+    static constexpr int k = 0, v = kTile, q = 2 * kTile, stage = 3 * kTile;
+    static constexpr int p = kStages * stage;                 // P pair [2][hi, lo]
+    static constexpr int out = p + 2 * 2 * kMat;
+    static constexpr int out_row = D * 2 + 16;
+    static constexpr int ring = out + C * out_row;            // alpha, gamma, w, mid of four blocks
+    static constexpr int bar = ring + 4 * 4 * C * 4;
+    static constexpr int bytes = bar + 256 + 1024;
+    // TMEM columns.  dS's first 64 hold the next block's Q K^T between two uses.
+    static constexpr uint32_t dS = 0, Sh = 128, O1 = 256, O2 = 320, V = 384;   // V: pairs of two blocks, 64 each
+    // Barriers.  Full: a block's tiles and decays are there.  BD, BQ, BP: dS, S^T Q^T, Q K^T done; BO:
+    // V^T P^T too.  CV, CP: diag(w) V, P are there; CD, CP0: dS, Q K^T are out of TMEM; CS: S's pair is
+    // there; CO: the readout is out of TMEM.  Where a waiter can be a block behind there are two.
+    enum { Full = 0, Empty = kStages, BD = 2 * kStages, BQ = BD + 2, BP, BO, CV = BO + 2, CP = CV + 2, CD = CP + 2,
+           CP0, CS, CO, Drain };
+};
+
+struct SegArgs {
+    int segs;                  // segments of a request (at most: short ones have fewer)
+    float* part;               // [n][H][segs][128][128]: state behind segment 0, sums of the others;
+                               // the last entry keeps the request's first state
+    float* decay;              // [n][H][segs] product of a segment's decays
+};
+
+template <bool SUM>
+__global__ void __launch_bounds__(EChain::threads, 1)
+    decay_chain_kernel(const ChunkArgs ca, const SegArgs sa, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using X = EChain;
+    const PrefillArgs& a = ca.p;
+    extern __shared__ __align__(1024) uint8_t sm_raw[];
+    const uint32_t base = (smem_u32(sm_raw) + 1023u) & ~1023u;
+    uint8_t* sm = sm_raw + (base - smem_u32(sm_raw));
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int seg = blockIdx.x % sa.segs, unit = blockIdx.x / sa.segs;
+    const int req = unit / a.H, h = unit % a.H;
+    const int end = min(max(__ldg(a.cu_seqlens + req + 1), 0), a.max_tokens);
+    const int first = min(max(__ldg(a.cu_seqlens + req), 0), end);
+    if (first == end) return;
+    const int blocks = (end - first + C - 1) / C, per = (blocks + sa.segs - 1) / sa.segs;
+    if (seg * per >= blocks || (SUM && (seg + 1) * per >= blocks)) return;   // nothing, or no one to hand on to
+    const bool last = (seg + 1) * per >= blocks;
+    const int start = first + seg * per * C, len = min(end - start, per * C), nc = (len + C - 1) / C;
+    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)start * a.H + h) * D;
+    if (slot < 0 || slot >= a.n_slots) {
+        if (SUM) return;
+        if (slot >= a.n_slots && tid == 0 && h == 0) atomicOr(a.status, DAMP_EFLAG_SLOT_RANGE);
+        for (long long e = tid; e < (long long)len * (D / 8); e += X::threads)
+            reinterpret_cast<uint4*>(out + (e / (D / 8)) * (size_t)a.H * D)[e % (D / 8)] =
+                make_uint4(0, 0, 0, 0);
+        return;
+    }
+    auto bar = [&](int i) { return base + X::bar + 8 * i; };
+
+    if (tid == 0) {
+        for (int i = 0; i < X::kStages; ++i) {
+            mbar_init(bar(X::Full + i), 2);
+            mbar_init(bar(X::Empty + i), 1 + X::kForm);
+        }
+        for (int i = X::BD; i < X::CV; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(X::CV + i), X::kForm);
+            mbar_init(bar(X::CP + i), X::kForm);
+        }
+        mbar_init(bar(X::CD), X::kWarps);
+        mbar_init(bar(X::CP0), X::kForm);
+        mbar_init(bar(X::CS), X::kWarps);
+        mbar_init(bar(X::CO), X::kOut);
+        mbar_init(bar(X::Drain), 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == X::wLoad) tmem_alloc(smem_u32(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    auto wait_all = [&](int i, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, bounded_wait(bar(i), parity, a.wait_ns, &s_abort, warp == X::wLoad));
+    };
+    auto wait_group = [&](bool polls, int i, uint32_t parity, int id, int threads) -> bool {
+        const bool ok = !polls || wait_all(i, parity);
+        return !bar_red_or(id, threads, !ok);
+    };
+    auto arrive = [&](int i) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(i));
+    };
+    const int quad = warp & 3;
+    const uint32_t lanes = tm + ((uint32_t)(quad * 32) << 16);
+    const int vcol = quad * 32 + lane;                 // a state or readout thread's value column
+    // alpha_t, gamma_t, gamma_C / gamma_t and (t >= 32) gamma_t / gamma_31 of block c
+    auto ring = [&](int c) { return reinterpret_cast<float*>(sm + X::ring) + (c & 3) * 4 * C; };
+
+    if (warp < X::kWarps) {
+        // ---------------------------------------------------------- state
+        const int part = warp >> 2;                    // key channels [32 part, +32)
+        const size_t at = (size_t)(part * 32) * D + vcol;
+        uint8_t* states = a.state + (size_t)h * D * D * 4;
+        float* parts = sa.part + (size_t)unit * sa.segs * D * D + at;
+        const bool has = from >= 0 && from < a.n_slots;
+        float S[32];
+        if (seg == 0) {
+            // the second pass may find the slot's new state in its place already
+            const float* in = !SUM && !last
+                ? parts + (size_t)(sa.segs - 1) * D * D
+                : reinterpret_cast<const float*>(states + (size_t)(a.state_by_slot ? (has ? from : slot) : req) *
+                                                              a.state_stride) + at;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = has ? in[(size_t)i * D] : 0.f;
+            if (SUM)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) parts[(size_t)(sa.segs - 1) * D * D + (size_t)i * D] = S[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = SUM ? 0.f : parts[(size_t)i * D];
+            if (!SUM)
+                for (int j = 1; j < seg; ++j) {
+                    const float g = sa.decay[(size_t)unit * sa.segs + j];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        S[i] = __fmaf_rn(g, S[i], parts[(size_t)j * D * D + (size_t)i * D]);
+                }
+        }
+        float total = 1.f;
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = c & 1;
+            if (!SUM) {
+                // ---- the state before block c as a pair
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split_bf16(S[2 * i], S[2 * i + 1], hi[i], lo[i]);
+                if (c > 0 && !(ok = wait_group(warp == 0, X::BQ, ph ^ 1, 4, X::kWarps * 32))) break;
+                tc_fence_after();
+                tmem_st16(lanes + X::Sh + part * 16, hi);
+                tmem_st16(lanes + X::Sh + 64 + part * 16, lo);
+                tmem_wait_st();
+                arrive(X::CS);
+            }
+            // ---- S <- gamma_C S + the block's part
+            if (!(ok = wait_group(warp == 0, X::BD + ph, (c >> 1) & 1, 4, X::kWarps * 32))) break;
+            tc_fence_after();
+            const float gc = ring(c)[2 * C - 1];
+            uint32_t y[32];
+            tmem_ld32(lanes + X::dS + part * 32, y);
+            tmem_wait_ld();
+            arrive(X::CD);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 s = __ffma2_rn(make_float2(gc, gc), make_float2(S[2 * i], S[2 * i + 1]),
+                                            make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
+                S[2 * i] = s.x;
+                S[2 * i + 1] = s.y;
+            }
+            total *= gc;
+        }
+        if (ok) {
+            if (SUM) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) parts[(size_t)seg * D * D + (size_t)i * D] = S[i];
+                if (tid == 0) sa.decay[(size_t)unit * sa.segs + seg] = total;
+            } else if (last) {
+                float* to = reinterpret_cast<float*>(
+                    states + (size_t)(a.state_by_slot ? slot : req) * a.state_stride) + at;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) to[(size_t)i * D] = S[i];
+            }
+        }
+    } else if (warp < X::wOut) {
+        // ---------------------------------------------------------- operands
+        constexpr int kId = 2, kN = X::kForm * 32;
+        const int ft = tid - X::kWarps * 32, c2 = (lane & 3) * 2;
+        // diag(w) V of block c as a pair in TMEM
+        auto form_v = [&](int c) -> bool {
+            const uint32_t st = base + c % X::kStages * X::stage, buf = c & 1;
+            const int live = min(C, len - c * C);
+            if (!wait_group(warp == X::kWarps, X::Full + c % X::kStages, (c / X::kStages) & 1, kId, kN)) return false;
+            if (live < C) {
+                // rows behind the end hold another request's keys and values: they must not
+                // enter the sums over tokens
+                uint8_t* stp = sm + c % X::kStages * X::stage;
+                for (int e = ft; e < (C - live) * 16; e += kN) {
+                    const int to = (e & 8 ? kHalf : 0) + (live + e / 16) * 128 + (e & 7) * 16;
+                    *reinterpret_cast<uint4*>(stp + X::k + to) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(stp + X::v + to) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            // the block before last has used this pair up
+            if (!wait_group(c >= 2 && warp == X::kWarps, X::BD + buf, ((c >> 1) - 1) & 1, kId, kN)) return false;
+            const float* w = ring(c) + 2 * C;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {   // 16 value columns (TMEM lanes) each, transposed by ldmatrix
+                uint32_t hi[16], lo[16];
+                const int col = quad * 32 + hf * 16;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // 16 tokens each
+                    uint32_t v[4];
+                    const int row = j * 16 + (lane & 7) + (lane >> 4) * 8;
+                    ldsm4t(v, st + X::v + (col >> 6) * kHalf +
+                                  swz(row, (col & 63) * 2 + ((lane >> 3) & 1) * 16));
+                    const float2 w0 = *reinterpret_cast<const float2*>(w + j * 16 + c2);
+                    const float2 w1 = *reinterpret_cast<const float2*>(w + j * 16 + 8 + c2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
+                        split_bf16(__fmul2_rn(x, i < 2 ? w0 : w1), hi[4 * j + i], lo[4 * j + i]);
+                    }
+                }
+                const uint32_t to = lanes + ((uint32_t)(hf * 16) << 16) + X::V + buf * 64;
+                tmem_st_16x128(to, hi);
+                tmem_st_16x128(to + 32, lo);
+            }
+            fence_proxy_async_smem();
+            tmem_wait_st();
+            arrive(X::CV + buf);
+            if (lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
+            return true;
+        };
+        bool ok = form_v(0) && (nc < 2 || form_v(1));
+        // this thread's token and its 32 columns of P (TMEM lanes 0..63: 0..31, 64..127: 32..63)
+        const int t = (quad & 1) * 32 + lane, s0 = (quad >> 1) * 32;
+        for (int c = 0; c < nc && ok; ++c) {
+            if (!SUM) {
+                uint8_t* pm = sm + X::p + (c & 1) * 2 * kMat;
+                if (!(ok = wait_group(warp == X::kWarps, X::BP, c & 1, kId, kN))) break;
+                tc_fence_after();
+                uint32_t y[32];
+                tmem_ld32(lanes + X::dS + s0, y);
+                tmem_wait_ld();
+                arrive(X::CP0);
+                const float* al = ring(c);
+                const bool row_live = t < min(C, len - c * C);
+                // gamma_t / gamma_s for s downwards; it starts at s = t, or from the columns above
+                float x = row_live && t >= s0 + 32 ? al[3 * C + t] : 0.f, above = 1.f;   // above: alpha_{s + 1}
+#pragma unroll
+                for (int j = 3; j >= 0; --j) {
+                    float f[8];
+                    const float4 a1 = *reinterpret_cast<const float4*>(al + s0 + j * 8 + 4);
+                    const float4 a0 = *reinterpret_cast<const float4*>(al + s0 + j * 8);
+                    const float as[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+                    for (int i = 7; i >= 0; --i) {
+                        x = s0 + j * 8 + i == t && row_live ? 1.f : x * above;
+                        above = as[i];
+                        f[i] = x == 0.f ? 0.f : x * __uint_as_float(y[j * 8 + i]);
+                    }
+                    uint4 hi, lo;
+                    split_bf16(f[0], f[1], hi.x, lo.x);
+                    split_bf16(f[2], f[3], hi.y, lo.y);
+                    split_bf16(f[4], f[5], hi.z, lo.z);
+                    split_bf16(f[6], f[7], hi.w, lo.w);
+                    const uint32_t to = swz(t, (s0 + j * 8) * 2);
+                    *reinterpret_cast<uint4*>(pm + to) = hi;
+                    *reinterpret_cast<uint4*>(pm + kMat + to) = lo;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(X::CP + (c & 1)));
+            }
+            if (c + 2 < nc) ok = form_v(c + 2);
+        }
+    } else if (warp < X::wLoad) {
+        // ---------------------------------------------------------- readout
+        const int wt = tid - X::wOut * 32;
+        uint8_t* so = sm + X::out;
+        for (int c = 0; c < (SUM ? 0 : nc); ++c) {
+            const float* gam = ring(c) + C;
+            if (!wait_group(warp == X::wOut, X::BO + (c & 1), (c >> 1) & 1, 1, X::kOut * 32)) break;
+            tc_fence_after();
+            // out of TMEM first: the next block's Q S waits for that
+            uint32_t o[C / 2];
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                uint32_t o1[16], o2[16];
+                tmem_ld16(lanes + X::O1 + part * 16, o1);
+                tmem_ld16(lanes + X::O2 + part * 16, o2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 gt = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
+                    o[part * 8 + i] = pack_bf16(
+                        __fmaf_rn(gt.x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
+                        __fmaf_rn(gt.y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
+                }
+            }
+            arrive(X::CO);
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) {
+                *reinterpret_cast<uint16_t*>(so + 2 * i * X::out_row + vcol * 2) = (uint16_t)o[i];
+                *reinterpret_cast<uint16_t*>(so + (2 * i + 1) * X::out_row + vcol * 2) = (uint16_t)(o[i] >> 16);
+            }
+            bar_sync(1, X::kOut * 32);
+            const int live = min(C, len - c * C);
+#pragma unroll
+            for (int i = 0; i < C * 16 / (X::kOut * 32); ++i) {
+                const int r = (wt >> 4) + i * (X::kOut * 2), u = wt & 15;
+                if (r < live)
+                    *reinterpret_cast<uint4*>(out + (size_t)(c * C + r) * a.H * D + u * 8) =
+                        *reinterpret_cast<const uint4*>(so + r * X::out_row + u * 16);
+            }
+            bar_sync(1, X::kOut * 32);
+        }
+    } else if (warp == X::wLoad) {
+        // ---------------------------------------------------------- loads
+        const int hq = h / (a.H / a.H_qk);
+        int issued = 0;
+        auto alpha_of = [&](int t) {
+            return t < len ? __ldg(a.alpha + (size_t)(start + t) * a.H + h) : 1.f;
+        };
+        float a0 = alpha_of(2 * lane), a1 = alpha_of(2 * lane + 1);    // of this lane's two tokens
+        for (int c = 0; c < nc; ++c) {
+            const int s = c % X::kStages;
+            if (c >= X::kStages && !wait_all(X::Empty + s, (c / X::kStages - 1) & 1)) break;
+            const uint32_t st = base + s * X::stage, f = bar(X::Full + s);
+            const int t = start + c * C;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(f, (SUM ? 2 : 3) * kTile);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    tma_load_3d(st + X::v + half * kHalf, &mv, half * 64, h, t, f);
+                    tma_load_3d(st + X::k + half * kHalf, &mk, half * 64, hq, t, f);
+                    if (!SUM) tma_load_3d(st + X::q + half * kHalf, &mq, half * 64, hq, t, f);
+                }
+            }
+            issued = c + 1;
+            // products of the decays up to each token, and behind it
+            float up = a0 * a1, down = up;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, up, off), w = __shfl_down_sync(0xffffffffu, down, off);
+                if (lane >= off) up = u * up;
+                if (lane + off < 32) down = down * w;
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 1.f;
+            if (lane == 31) behind = 1.f;
+            float mid = a0 * a1;               // from token 32 on
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, mid, off);
+                if (lane >= 16 + off) mid = u * mid;
+            }
+            float mid0 = __shfl_up_sync(0xffffffffu, mid, 1);
+            mid0 = lane == 16 ? a0 : mid0 * a0;
+            float2* r = reinterpret_cast<float2*>(ring(c)) + lane;
+            r[0] = make_float2(a0, a1);
+            r[C / 2] = make_float2(before * a0, up);
+            r[C] = make_float2(a1 * behind, behind);
+            r[3 * C / 2] = make_float2(mid0, mid);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(f);
+            a0 = alpha_of((c + 1) * C + 2 * lane);
+            a1 = alpha_of((c + 1) * C + 2 * lane + 1);
+        }
+        // copies in flight end before the CTA does
+        for (int c = max(0, issued - X::kStages); c < issued; ++c)
+            mbar_wait_bounded(bar(X::Full + c % X::kStages), (c / X::kStages) & 1, a.wait_ns);
+    } else {
+        // ---------------------------------------------------------- matrix instructions
+        constexpr uint32_t ids = mma_idesc(128, 128, false, true), idk = mma_idesc(128, 64, false, false),
+                           idv = mma_idesc(128, 64, true, false), idp = mma_idesc(128, 32, false, false);
+        auto scores = [&](int c) -> bool {           // Q K^T of block c
+            const uint32_t st = base + c % X::kStages * X::stage;
+            if (!wait_all(X::Full + c % X::kStages, (c / X::kStages) & 1)) return false;
+            if (elect_one()) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)     // columns; rows of M that are not Q's are not used
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss(tm + X::dS + half * 32,
+                               desc_k_major(st + X::q - half * kHalf + (ks >> 2) * kHalf + (ks & 3) * 32),
+                               desc_k_major(st + X::k + (ks >> 2) * kHalf + half * (kHalf / 2) + (ks & 3) * 32), idp,
+                               ks > 0);
+                tc_commit(bar(X::BP));
+            }
+            return true;
+        };
+        bool ok = SUM || scores(0);
+        for (int c = 0; c < nc && ok; ++c) {
+            const uint32_t st = base + c % X::kStages * X::stage, ph = c & 1;
+            if (!(ok = wait_all(X::CV + ph, (c >> 1) & 1))) break;     // (its writers saw the stage full)
+            if (SUM && c > 0 && !(ok = wait_all(X::CD, ph ^ 1))) break;
+            if (!SUM && !(ok = wait_all(X::CP0, ph))) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(tm + X::dS, tm + X::V + ph * 64 + 8 * ks,
+                           desc_mn_major(st + X::k + (ks & 3) * 2048, kHalf), ids, ks > 0);
+                tc_commit(bar(X::BD + ph));
+                if (SUM) tc_commit(bar(X::Empty + c % X::kStages));
+            }
+            if (SUM) continue;
+            if (c > 0 && !(ok = wait_all(X::CO, ph ^ 1))) break;
+            if (!(ok = wait_all(X::CS, ph))) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 16; ++ks)
+                    mma_ts(tm + X::O1, tm + X::Sh + 8 * ks,
+                           desc_k_major(st + X::q + ((ks >> 2) & 1) * kHalf + (ks & 3) * 32), idk, ks > 0);
+                tc_commit(bar(X::BQ));
+            }
+            if (c + 1 < nc) {
+                if (!(ok = wait_all(X::CD, ph))) break;
+                tc_fence_after();
+                if (!(ok = scores(c + 1))) break;
+            }
+            if (!(ok = wait_all(X::CP + ph, (c >> 1) & 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t pm = base + X::p + ph * 2 * kMat;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ss(tm + X::O2, desc_mn_major(st + X::v + (ks & 3) * 2048, kHalf),
+                           desc_k_major(pm + (ks >> 2) * kMat + (ks & 3) * 32), idv, ks > 0);
+                tc_commit(bar(X::BO + ph));
+                tc_commit(bar(X::Empty + c % X::kStages));
+            }
+        }
+        // nothing in flight when TMEM and shared memory are given back
+        if (elect_one()) tc_commit(bar(X::Drain));
+        mbar_wait_bounded(bar(X::Drain), 0, a.wait_ns);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
+    if (warp == X::wLoad) {
+        tc_fence_after();
+        tmem_free(tm, 512);
+    }
+}
+
 // ------------------------------------------------------------------ host
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1461,23 +1285,15 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int heads, long long rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool DELTA>
-cudaError_t set_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(prepare_kernel<DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PrepSmem<DELTA>::bytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(chain_kernel<DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                ChainSmem<DELTA>::bytes);
-}
-
-template <bool DELTA>
-cudaError_t launch_rule(const ChunkArgs& ca, const CUtensorMap& mq, const CUtensorMap& mk,
-                        const CUtensorMap& mv, cudaStream_t s) {
-    prepare_kernel<DELTA><<<dim3(ca.p.max_blocks, ca.p.H), kPrepThreads, PrepSmem<DELTA>::bytes, s>>>(ca);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    chain_kernel<DELTA><<<ca.p.n * ca.p.H, kChainThreads, ChainSmem<DELTA>::bytes, s>>>(ca, mq, mk, mv);
-    return cudaGetLastError();
+// Segments of a request for the decay rule: enough for two thirds of the SMs
+// or more to have one, none shorter (on average) than 4 blocks; a batch whose
+// (request, head) pairs fill the SMs stays whole (the first pass reads K and V
+// once more: +50 % bytes).  TODO measured
+int decay_segments(int n, int H, int max_tokens, int sms) {
+    const long long chains = (long long)n * H;
+    if (chains * 2 > sms) return 1;
+    const long long blocks = max_tokens / ((long long)C * n);
+    return (int)std::max(1ll, std::min((long long)sms / chains, blocks / 4));
 }
 
 size_t first_block_bytes(int n) { return ((size_t)n * 4 + 255) / 256 * 256; }
@@ -1497,24 +1313,43 @@ cudaError_t prepare_prefill() {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  DChain::bytes);
-    return e != cudaSuccess ? e : set_attributes<false>();
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decay_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 EChain::bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decay_chain_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 EChain::bytes);
+    return e;
 }
 
 bool prefill_chunk_fits(int d_k, int d_v, int bf16) { return bf16 && d_k == D && d_v == D; }
 
-size_t prefill_chunk_bytes(int n, int H, int max_blocks, int delta) {
-    return first_block_bytes(n) +
-           (size_t)max_blocks * H * (delta ? DRec::bytes : Rec<false>::bytes);
+size_t prefill_chunk_bytes(int n, int H, int max_tokens, int max_blocks, int delta) {
+    if (delta) return first_block_bytes(n) + (size_t)max_blocks * H * DRec::bytes;
+    const int segs = decay_segments(n, H, max_tokens, kSms);
+    return segs == 1 ? 0 : (size_t)n * H * segs * (D * D + 1) * 4;
 }
 
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
-    ChunkArgs ca{a, reinterpret_cast<int32_t*>(a.work), a.work + first_block_bytes(a.n)};
     CUtensorMap mq, mk, mv;
     cudaError_t e = token_map(&mq, a.q, a.H_qk, a.max_tokens, a.q_stride);
     if (e == cudaSuccess) e = token_map(&mk, a.k, a.H_qk, a.max_tokens, a.k_stride);
     if (e == cudaSuccess) e = token_map(&mv, a.v, a.H, a.max_tokens, a.v_stride);
     if (e != cudaSuccess) return e;
-    if (!a.delta) return launch_rule<false>(ca, mq, mk, mv, s);
+    ChunkArgs ca{a, nullptr, nullptr};
+    if (!a.delta) {
+        SegArgs sa{decay_segments(a.n, a.H, a.max_tokens, kSms), reinterpret_cast<float*>(a.work), nullptr};
+        sa.decay = sa.part + (size_t)a.n * a.H * sa.segs * D * D;
+        const int grid = a.n * a.H * sa.segs;
+        if (sa.segs > 1) {
+            decay_chain_kernel<true><<<grid, EChain::threads, EChain::bytes, s>>>(ca, sa, mq, mk, mv);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+        decay_chain_kernel<false><<<grid, EChain::threads, EChain::bytes, s>>>(ca, sa, mq, mk, mv);
+        return cudaGetLastError();
+    }
+    ca.first_block = reinterpret_cast<int32_t*>(a.work);
+    ca.records = a.work + first_block_bytes(a.n);
     delta_prepare_kernel<<<a.max_blocks * a.H, kPrepThreads, DPrep::bytes, s>>>(ca);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     delta_chain_kernel<<<a.n * a.H, DChain::threads, DChain::bytes, s>>>(ca, mq, mk, mv);
