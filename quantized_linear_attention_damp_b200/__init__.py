@@ -411,6 +411,32 @@ class _on_device:
             self.guard.__exit__(*exc)
 
 
+def _want(t, name: str, shape: tuple, dtype, device=None):
+    """One tensor argument: shape, type, contiguity, and the device of the
+    call's other tensors.  Returns its address."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"tensors on different devices: {device} and {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _launch_stream(stream, device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    return _stream(stream, device)
+
+
 def _alloc_stream(stream, device):
     """Context in which torch allocates (and fills) on ``stream``."""
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
@@ -418,13 +444,12 @@ def _alloc_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _in_dtype(q, k, v) -> int:
-    _cuda(q, None, "q")
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("q, k, v must be bfloat16 or float32")
-    _cuda(k, q.dtype, "k")
-    _cuda(v, q.dtype, "v")
-    return DAMP_DTYPE_BF16 if q.dtype == torch.bfloat16 else DAMP_DTYPE_F32
+def _in_dtype(q) -> int:
+    if q.dtype is torch.bfloat16:
+        return DAMP_DTYPE_BF16
+    if q.dtype is torch.float32:
+        return DAMP_DTYPE_F32
+    raise ValueError("q, k, v must be bfloat16 or float32")
 
 
 def _shared_heads(q, H: int, n: int, d_k: int) -> int:
@@ -446,19 +471,13 @@ def damp_decay_step(pool: int, slot_idx: torch.Tensor, q: torch.Tensor, k: torch
         raise ValueError("slot_idx must be a 1-D tensor")
     n = slot_idx.numel()
     H_qk = _shared_heads(q, H, n, d_k)
-    _shape(q, "q", (n, H_qk, d_k))
-    _shape(k, "k", (n, H_qk, d_k))
-    _shape(v, "v", (n, H, d_v))
-    _shape(alpha, "alpha", (n, H))
-    _shape(out, "out", (n, H, d_v))
-    _cuda(slot_idx, torch.int32, "slot_idx")
-    dt = _in_dtype(q, k, v)
-    _cuda(alpha, torch.float32, "alpha")
-    _cuda(out, torch.float32, "out")
-    _same_device(stream, slot_idx, q, k, v, alpha, out)
-    with _on_device(q.device):
-        _check(_lib.damp_decay_step(pool, n, _ptr(slot_idx), dt, H_qk, _ptr(q), _ptr(k), _ptr(v),
-                                    _ptr(alpha), _ptr(out), _stream(stream, q.device)),
+    dt, kind, dev = _in_dtype(q), q.dtype, q.device
+    f32 = torch.float32
+    ptr = (_want(slot_idx, "slot_idx", (n,), torch.int32, dev), _want(q, "q", (n, H_qk, d_k), kind),
+           _want(k, "k", (n, H_qk, d_k), kind, dev), _want(v, "v", (n, H, d_v), kind, dev),
+           _want(alpha, "alpha", (n, H), f32, dev), _want(out, "out", (n, H, d_v), f32, dev))
+    with _on_device(dev):
+        _check(_lib.damp_decay_step(pool, n, ptr[0], dt, H_qk, *ptr[1:], _launch_stream(stream, dev)),
                "damp_decay_step")
 
 
@@ -482,26 +501,22 @@ def damp_batch_plan(lengths: torch.Tensor, slot_idx: torch.Tensor, past, n_slots
     if not isinstance(lengths, torch.Tensor) or lengths.dim() != 1:
         raise ValueError("lengths must be a 1-D tensor")
     n = lengths.numel()
-    blocks = damp_plan_blocks(n, max_tokens)
-    named = {"lengths": (lengths, (n,)), "slot_idx": (slot_idx, (n,)),
-             "cu_seqlens": (cu_seqlens, (n + 1,)), "load_slot": (load_slot, (n,)),
-             "store_slot": (store_slot, (n,)), "block_table": (block_table, (blocks, 4)),
-             "totals": (totals, (4,))}
-    if past is not None:
-        named["past"] = (past, (n,))
-    if token_slot is not None or token_pos is not None:
-        named["token_slot"] = (token_slot, (max_tokens,))
-        named["token_pos"] = (token_pos, (max_tokens,))
-    for name, (t, shape) in named.items():
-        _shape(t, name, shape)
-        _cuda(t, torch.int32, name)
-    _same_device(stream, *(t for t, _ in named.values()))
-    with _on_device(lengths.device):
-        _check(_lib.damp_batch_plan(n, _ptr(lengths), _ptr(past), _ptr(slot_idx), n_slots,
-                                    max_tokens, _ptr(cu_seqlens), _ptr(load_slot),
-                                    _ptr(store_slot), _ptr(block_table), _ptr(token_slot),
-                                    _ptr(token_pos), _ptr(totals),
-                                    _stream(stream, lengths.device)), "damp_batch_plan")
+    dev, i32 = lengths.device, torch.int32
+    if (token_slot is None) != (token_pos is None):
+        raise ValueError("token_slot and token_pos go together")
+    ptr = (_want(lengths, "lengths", (n,), i32),
+           None if past is None else _want(past, "past", (n,), i32, dev),
+           _want(slot_idx, "slot_idx", (n,), i32, dev))
+    outs = (_want(cu_seqlens, "cu_seqlens", (n + 1,), i32, dev),
+            _want(load_slot, "load_slot", (n,), i32, dev),
+            _want(store_slot, "store_slot", (n,), i32, dev),
+            _want(block_table, "block_table", (damp_plan_blocks(n, max_tokens), 4), i32, dev),
+            None if token_slot is None else _want(token_slot, "token_slot", (max_tokens,), i32, dev),
+            None if token_pos is None else _want(token_pos, "token_pos", (max_tokens,), i32, dev),
+            _want(totals, "totals", (4,), i32, dev))
+    with _on_device(dev):
+        _check(_lib.damp_batch_plan(n, *ptr, n_slots, max_tokens, *outs, _launch_stream(stream, dev)),
+               "damp_batch_plan")
 
 
 def damp_prefill_workspace(pool: int, rule: int, n: int, max_tokens: int, in_dtype: int) -> int:
@@ -533,45 +548,40 @@ def damp_prefill(pool: int, rule: int, cu_seqlens: torch.Tensor, load_slot: torc
     _, _, H, d_k, d_v = _pool_shape(pool)
     n = load_slot.numel()
     H_qk = _shared_heads(q, H, q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0, d_k)
-    T = q.shape[0]
+    T, kind, dev = q.shape[0], q.dtype, q.device
     if rule not in (DAMP_RULE_DELTA, DAMP_RULE_DECAY):
         raise ValueError(f"unknown rule {rule}")
-    _shape(q, "q", (T, H_qk, d_k))
-    _shape(k, "k", (T, H_qk, d_k))
-    _shape(v, "v", (T, H, d_v))
-    _shape(alpha, "alpha", (T, H))
-    _shape(out, "out", (T, H, d_v))
-    dt = _in_dtype(q, k, v)
-    _cuda(alpha, torch.float32, "alpha")
-    _cuda(out, q.dtype, "out")
-    ints = (("cu_seqlens", cu_seqlens, (n + 1,)), ("load_slot", load_slot, (n,)),
-            ("store_slot", store_slot, (n,)),
-            ("block_table", block_table, (damp_plan_blocks(n, T), 4)))
-    for name, t, shape in ints:
-        _shape(t, name, shape)
-        _cuda(t, torch.int32, name)
     if (beta is not None) != (rule == DAMP_RULE_DELTA):
         raise ValueError("beta goes with the delta rule, and only with it")
-    if beta is not None:
-        _shape(beta, "beta", (T, H))
-        _cuda(beta, torch.float32, "beta")
-    _same_device(stream, q, k, v, alpha, out, cu_seqlens, load_slot, store_slot, block_table,
-                 *(t for t in (beta, workspace) if t is not None))
-    strides = [_token_stride(t, name) for t, name in ((q, "q"), (k, "k"), (v, "v"))]
-    with _on_device(q.device):
-        need = damp_prefill_workspace(pool, rule, n, T, dt)
-        handle = _stream(stream, q.device)
-        if workspace is not None:
-            _cuda(workspace, torch.uint8, "workspace")
-        elif need:
+    dt, f32, i32 = _in_dtype(q), torch.float32, torch.int32
+    rows = []
+    for t, name, shape in ((q, "q", (T, H_qk, d_k)), (k, "k", (T, H_qk, d_k)), (v, "v", (T, H, d_v))):
+        _shape(t, name, shape)
+        _cuda(t, kind, name)
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+        rows += [t.data_ptr(), _token_stride(t, name)]
+    ints = (_want(cu_seqlens, "cu_seqlens", (n + 1,), i32, dev),
+            _want(load_slot, "load_slot", (n,), i32, dev),
+            _want(store_slot, "store_slot", (n,), i32, dev),
+            _want(block_table, "block_table", (damp_plan_blocks(n, T), 4), i32, dev))
+    ends = (_want(alpha, "alpha", (T, H), f32, dev),
+            None if beta is None else _want(beta, "beta", (T, H), f32, dev),
+            _want(out, "out", (T, H, d_v), kind, dev))
+    with _on_device(dev):
+        handle = _launch_stream(stream, dev)
+        need, space = damp_prefill_workspace(pool, rule, n, T, dt), None
+        if workspace is None and need:
             # the launch's stream owns it: the memory is given out again only
             # behind this call's work
-            with _alloc_stream(stream, q.device):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _check(_lib.damp_prefill(pool, rule, n, T, _ptr(cu_seqlens), _ptr(load_slot),
-                                 _ptr(store_slot), _ptr(block_table), dt, H_qk, q.data_ptr(),
-                                 strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
-                                 _ptr(alpha), _ptr(beta), _ptr(out), _ptr(workspace),
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                with _alloc_stream(stream, dev):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            space = _want(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        _check(_lib.damp_prefill(pool, rule, n, T, *ints, dt, H_qk, *rows, *ends, space,
                                  0 if workspace is None else workspace.numel(), handle),
                "damp_prefill")
 
