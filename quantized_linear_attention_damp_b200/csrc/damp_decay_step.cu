@@ -116,7 +116,10 @@ __global__ void __launch_bounds__(kDecayThreads) decay_step_kernel(const StepArg
 // 8 rows, not 8 by every lane.
 //   SOLO: a warp owns a unit and all its batches; no barrier, no sum over
 //   warps.  Otherwise the 8 warps of a CTA share a unit.
-// MEASURED
+// Measured at 512 x 48 states of 128 x 128: mixed 227 us (4.5 TB/s, 69 % of the
+// copy rate), INT8 225, FP8 233; the tile kernel above took 894 (one CTA an SM
+// at 134 registers).  What bounds it is issue: dequantizing, two roundings and
+// requantizing cost about 55 instructions a row of 128 values.
 //
 // KIND: 0 FP32, 1 INT8 (and FP16) rows, 2 FP8 rows.  ALL: every lane holds
 // columns (d_v = 128 G).
@@ -410,8 +413,9 @@ cudaError_t launch_rows_t(const StepArgs& a, int H_qk, int bf16, cudaStream_t s)
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int units = a.n * a.H, ctas = sms * (G == 1 ? 3 : 2), warps = kDecayThreads / 32;
     const bool all = a.d_v == 128 * G;
-    // a warp per unit needs a few units for every warp, or the last ones run alone
-    if (units >= 2 * ctas * warps)
+    // A warp per unit once two thirds of the warps have one (128 x 32 mixed d = 128 states 48.0 us
+    // against 57.4 for a CTA per unit, 64 x 32: 35.7 against 32.3).
+    if (units * 3ll >= 2ll * ctas * warps)
         return all ? launch_rows_f<KIND, G, true, true>(a, ctas, H_qk, bf16, s)
                    : launch_rows_f<KIND, G, true, false>(a, ctas, H_qk, bf16, s);
     return all ? launch_rows_f<KIND, G, false, true>(a, std::min(units, ctas), H_qk, bf16, s)
