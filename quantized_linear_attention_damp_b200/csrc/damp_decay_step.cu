@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(kDecayThreads, G == 1 ? 3 : 2)
                     float mine = 0.f;          // lane i: row i's largest magnitude
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const float s = BYTE ? reinterpret_cast<const float*>(sl + G * 2048)[i0 + i] : 0.f;
+                        [[maybe_unused]] const float s =
+                            BYTE ? reinterpret_cast<const float*>(sl + G * 2048)[i0 + i] : 0.f;
 #pragma unroll
                         for (int c = 0; c < G; ++c) {
                             y[i][c][0] = y[i][c][1] = make_float2(0.f, 0.f);

@@ -59,27 +59,12 @@ struct ChunkArgs {
 
 // ------------------------------------------------------------------ prepare
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 constexpr int kPrepThreads = 128;
-constexpr int kRowB = (D + 8) * 2;     // bytes of a staged Q or K row (8 extra values: no bank conflicts)
 
 constexpr int kTile = C * D * 2;       // bytes of a Q, K or V tile: two halves of 64 channels
 constexpr int kHalf = kTile / 2;
@@ -107,10 +92,15 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 
 // ------------------------------------------------------------------ delta: prepare
 //
-// 128 threads a (block, head), five CTAs an SM: the steps are short and each
-// waits for the one before, so it is the number of resident CTAs that keeps the
-// SM busy.  Q and K share their 34 KB with A and T (FP32) and then with the
-// finished record.
+// 128 threads a (block, head), four CTAs an SM (TMEM: 128 columns each): the
+// steps are short and each waits for the one before, so it is the number of
+// resident CTAs that keeps the SM busy.  [Q; K] K^T is one tensor-core product
+// of 128 rows; a thread then has one row of Q K^T (warps 0, 1) or K K^T (warps
+// 2, 3) and multiplies the decays up along it.  P = Q K^T o Gamma goes back to
+// TMEM as the A operand of G = P T'.  The inverse is FP32 arithmetic of the
+// ordinary kind: an error of it is an error of the state.  Q and K share their
+// 32 KB with A and T (FP32) and then with the finished record.
+// (Products by mma.sync, staged by the threads: 97 us for 4096 units, MEASURED.)
 
 // The record of one (block, head): C x C bf16 matrices with 128-byte rows
 // (K-major, 128-byte swizzle) in the order in which the chain's products take
@@ -123,154 +113,161 @@ struct DRec {
 
 constexpr int kFA = C + 4;             // floats of a row of A and T
 struct DPrep {
-    static constexpr int q = 0, k = C * kRowB;
-    static constexpr int a = 0, t = C * kFA * 4;       // over q and k
-    static constexpr int img = 0;                      // over a and t
-    static constexpr int dia = 2 * C * kRowB;          // Gamma of the diagonal 16 x 16 blocks [4][16][16]
-    static constexpr int vec = dia + 4 * 16 * 16 * 4;  // alpha, beta, pre, post, gamma, w
-    static constexpr int bytes = vec + 6 * C * 4 + 32;
-    static_assert(C * kFA * 4 <= C * kRowB, "A fits over Q, T over K");
-    static_assert(DRec::bytes <= 2 * C * kRowB, "the record fits over Q and K");
+    static constexpr int qk = 0;                       // Q0 K0 Q1 K1: halves of 64 channels
+    static constexpr int a = 0, t = C * kFA * 4;       // over Q and K
+    static constexpr int img = 0;                      // over A and T
+    static constexpr int vec = 2 * C * kFA * 4;        // alpha, beta, gamma, w
+    static constexpr int bytes = vec + 4 * C * 4 + 1024;
+    static_assert(2 * kTile <= vec && DRec::bytes <= vec, "Q and K, and the record, fit over A and T");
+    // TMEM: [Q; K] K^T, then P hi, lo (32 columns each); G
+    static constexpr uint32_t tQK = 0, tP = 0, tG = 64, cols = 128;
 };
 
-__global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(const ChunkArgs ca) {
+__global__ void __launch_bounds__(kPrepThreads, 4)
+    delta_prepare_kernel(const ChunkArgs ca, const __grid_constant__ CUtensorMap mq,
+                         const __grid_constant__ CUtensorMap mk) {
     const PrefillArgs& a = ca.p;
-    extern __shared__ __align__(1024) uint8_t sm[];
-    const int tid = threadIdx.x, lane = tid & 31;
+    extern __shared__ __align__(1024) uint8_t sm_raw[];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ __align__(8) uint64_t s_bar[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // heads of a block run side by side: their rows of Q and K are neighbours in memory
     const int blk = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int4 row = __ldg(reinterpret_cast<const int4*>(a.block_table) + blk);
     const int req = row.x, t0 = row.y, len = row.z;
-    // the triangles give the later row groups more work: a different warp has them in each CTA,
-    // or one scheduler of the SM would do most of it
-    const int warp = ((tid >> 5) + blk + h) & 3;
     if (req < 0 || req >= a.n || t0 < 0 || len < 1 || len > C || t0 > a.max_tokens - len) return;
     if (h == 0 && row.w == 0 && tid == 0) ca.first_block[req] = blk;
     const int slot = __ldg(a.store_slot + req);
     if (slot < 0 || slot >= a.n_slots) return;
-    const int hq = h / (a.H / a.H_qk);
-    float* s_dia = reinterpret_cast<float*>(sm + DPrep::dia);
+    const uint32_t base = (smem_u32(sm_raw) + 1023u) & ~1023u;
+    uint8_t* sm = sm_raw + (base - smem_u32(sm_raw));
     float* s_al = reinterpret_cast<float*>(sm + DPrep::vec);
     float* s_be = s_al + C;
-    float* s_pre = s_al + 2 * C;     // product of alpha from the 16-token group's start to t
-    float* s_post = s_al + 3 * C;    // product of alpha behind s to its group's end
-    float* s_ga = s_al + 4 * C;
-    float* s_w = s_al + 5 * C;
+    float* s_ga = s_al + 2 * C;
+    float* s_w = s_al + 3 * C;
+    const uint32_t bar_in = smem_u32(&s_bar[0]), bar_mma = smem_u32(&s_bar[1]);
 
-    // ---- Q and K rows (zeros behind the request's end), decays
-    {
-        const uint16_t* qg = static_cast<const uint16_t*>(a.q) + (size_t)t0 * a.q_stride + (size_t)hq * D;
-        const uint16_t* kg = static_cast<const uint16_t*>(a.k) + (size_t)t0 * a.k_stride + (size_t)hq * D;
-        const int r = tid >> 4, c = tid & 15;
-        uint4 kv[C / 8], qv[C / 8];
+    if (warp == 0) {
+        if (elect_one()) {
+            mbar_init(bar_in, 1);
+            mbar_init(bar_mma, 1);
+            fence_mbar_init();
+            s_abort = 0;
+            const int hq = h / (a.H / a.H_qk);
+            mbar_arrive_expect_tx(bar_in, 2 * kTile);
 #pragma unroll
-        for (int i = 0; i < C / 8; ++i) {
-            const int at = r + 8 * i;
-            kv[i] = qv[i] = make_uint4(0, 0, 0, 0);
-            if (at < len) {
-                kv[i] = __ldg(reinterpret_cast<const uint4*>(kg + (size_t)at * a.k_stride) + c);
-                qv[i] = __ldg(reinterpret_cast<const uint4*>(qg + (size_t)at * a.q_stride) + c);
+            for (int half = 0; half < 2; ++half) {
+                tma_load_3d(base + DPrep::qk + half * kTile, &mq, half * 64, hq, t0, bar_in);
+                tma_load_3d(base + DPrep::qk + half * kTile + kHalf, &mk, half * 64, hq, t0, bar_in);
             }
         }
-        if (tid < C) {
-            s_al[tid] = tid < len ? __ldg(a.alpha + (size_t)(t0 + tid) * a.H + h) : 1.f;
-            s_be[tid] = tid < len ? __ldg(a.beta + (size_t)(t0 + tid) * a.H + h) : 0.f;
-        }
+        __syncwarp();
+        tmem_alloc(smem_u32(&s_tmem), DPrep::cols);
+    } else if (warp == 1) {
+        // decays, two tokens a lane: as they are, their products up to each token and behind it
+        const float* al = a.alpha + (size_t)t0 * a.H + h;
+        const float* be = a.beta + (size_t)t0 * a.H + h;
+        const int i = 2 * lane;
+        const float a0 = i < len ? __ldg(al + (size_t)i * a.H) : 1.f;
+        const float a1 = i + 1 < len ? __ldg(al + (size_t)(i + 1) * a.H) : 1.f;
+        const float b0 = i < len ? __ldg(be + (size_t)i * a.H) : 0.f;
+        const float b1 = i + 1 < len ? __ldg(be + (size_t)(i + 1) * a.H) : 0.f;
+        float up = a0 * a1, down = up;
 #pragma unroll
-        for (int i = 0; i < C / 8; ++i) {
-            *reinterpret_cast<uint4*>(sm + DPrep::k + (r + 8 * i) * kRowB + c * 16) = kv[i];
-            *reinterpret_cast<uint4*>(sm + DPrep::q + (r + 8 * i) * kRowB + c * 16) = qv[i];
+        for (int off = 1; off < 32; off <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, up, off), d = __shfl_down_sync(0xffffffffu, down, off);
+            if (lane >= off) up = u * up;
+            if (lane + off < 32) down = down * d;
         }
+        float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+        if (lane == 0) before = 1.f;
+        if (lane == 31) behind = 1.f;
+        reinterpret_cast<float2*>(s_al)[lane] = make_float2(a0, a1);
+        reinterpret_cast<float2*>(s_be)[lane] = make_float2(b0, b1);
+        reinterpret_cast<float2*>(s_ga)[lane] = make_float2(before * a0, up);
+        reinterpret_cast<float2*>(s_w)[lane] = make_float2(a1 * behind, behind);
     }
+    tc_fence_before();
     __syncthreads();
-    // Gamma_ts inside a group of 16 tokens by running products down column s;
-    // between groups I > J it is pre_t * (whole groups between) * post_s
-    if (tid < C + 4) {
-        const int g0 = tid < C ? tid & ~15 : (tid - C) * 16, s = tid < C ? tid & 15 : -1;
-        float al[16], x = 1.f;
-#pragma unroll
-        for (int t = 0; t < 16; t += 4)
-            *reinterpret_cast<float4*>(al + t) = *reinterpret_cast<const float4*>(s_al + g0 + t);
-        float* to = tid < C ? s_dia + g0 * 16 + s : s_pre + g0;
-        const int step = tid < C ? 16 : 1;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            x = t > s ? x * al[t] : x;
-            if (t >= s) to[t * step] = x;
-        }
-        if (tid < C) s_post[tid] = x;
-    }
+    tc_fence_after();
+    const uint32_t tm = s_tmem, lanes = tm + ((uint32_t)(warp * 32) << 16);
 
-    // ---- Q K^T and K K^T: warp w has rows [16 w, 16 w + 16), columns up to its diagonal
-    const uint32_t base = smem_u32(sm);
-    const int r0 = warp * 16, g = lane >> 2, c2 = (lane & 3) * 2;
-    float P[8][4], M[8][4];
+    // ---- [Q; K] K^T
+    bool ok = true;
+    if (warp == 0) {
+        ok = __all_sync(0xffffffffu, bounded_wait(bar_in, 0, a.wait_ns, &s_abort, false));
+        if (ok && len < C) {
+            // rows behind the request's end hold another request's keys, NaN for all we know
+            for (int e = lane; e < (C - len) * 16; e += 32)
+                *reinterpret_cast<uint4*>(sm + DPrep::qk + (e & 8 ? kTile : 0) + kHalf + (len + e / 16) * 128 +
+                                          (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        if (ok && elect_one()) {
+            constexpr uint32_t id = mma_idesc(128, 64, false, false);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) P[j][i] = M[j][i] = 0.f;
-    {
-        const uint32_t a_off = base + (r0 + (lane & 15)) * kRowB + (lane >> 4) * 16;
-        const uint32_t b_off = base + DPrep::k + ((lane & 7) + (lane >> 4) * 8) * kRowB + ((lane >> 3) & 1) * 16;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t qa[4], ka[4];
-            ldsm4(qa, a_off + DPrep::q + ks * 32);
-            ldsm4(ka, a_off + DPrep::k + ks * 32);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {      // two column tiles at a time
-                if (j > warp) break;
-                uint32_t b[4];
-                ldsm4(b, b_off + j * 16 * kRowB + ks * 32);
-                mma16816(P[2 * j], qa, b[0], b[1]);
-                mma16816(P[2 * j + 1], qa, b[2], b[3]);
-                mma16816(M[2 * j], ka, b[0], b[1]);
-                mma16816(M[2 * j + 1], ka, b[2], b[3]);
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t at = base + DPrep::qk + (ks >> 2) * kTile + (ks & 3) * 32;
+                mma_ss(tm + DPrep::tQK, desc_k_major(at), desc_k_major(at + kHalf), id, ks > 0);
             }
+            tc_commit(bar_mma);
         }
     }
-    __syncthreads();                       // the decays are there; Q and K are used up
-
-    // ---- P = Q K^T o Gamma (registers), A = diag(beta) K K^T o Gamma below the diagonal (shared)
+    ok = ok && bounded_wait(bar_mma, 0, a.wait_ns, &s_abort, false);
+    const bool fine = __syncthreads_and(ok);       // (a wait that ran out: nothing more is done)
+    tc_fence_after();
     float* s_a = reinterpret_cast<float*>(sm + DPrep::a);
     float* s_t = reinterpret_cast<float*>(sm + DPrep::t);
-    // whole-group products: all[J] = alpha over group J
-    const float all1 = s_pre[31], all2 = s_pre[47];
+    const int r0 = warp * 16;
+    if (fine) {
+        // ---- row t of P (to TMEM as a pair) or of A = diag(beta) K K^T o Gamma below the diagonal
+        const int t = (warp & 1) * 32 + lane;
+        const bool is_p = warp < 2;
+        // gamma_t / gamma_s from s = t down (times beta_t for A), zero above; rows of P behind the
+        // request's end are used by no one
+        const float first = is_p ? 1.f : s_be[t];
+        float x = 0.f, above = 1.f;                // above: alpha_{s + 1}
+        uint32_t hi[2][16] = {}, lo[2][16] = {};
 #pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-        const int t = r0 + g + 8 * i2;
-        const float be = s_be[t], pre = s_pre[t];
-        const bool row_live = t < len;
+        for (int part = 1; part >= 0; --part) {
+            if (part > (warp & 1)) continue;       // above the diagonal: P stays zero, A is not read
+            uint32_t y[32];
+            tmem_ld32(lanes + DPrep::tQK + part * 32, y);
+            tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int J = j >> 1;
-            if (J > warp) break;           // above the diagonal: P stays zero, A is not read
-            // decay from the end of group J to the start of this warp's group
-            const float mid = J + 1 >= warp ? 1.f
-                              : (J == 0 ? (warp == 2 ? all1 : all1 * all2) : all2);
+            for (int j = 7; j >= 0; --j) {
+                const float4 av = *reinterpret_cast<const float4*>(s_al + part * 32 + j * 4);
+                const float as[4] = {av.x, av.y, av.z, av.w};
+                float f[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int s = 8 * j + c2 + i;
-                float dec;
-                if (J == warp) dec = s <= t ? s_dia[t * 16 + (s & 15)] : 0.f;
-                else dec = pre * (mid * s_post[s]);
-                if (!row_live) dec = 0.f;
-                const float m = M[j][2 * i2 + i];
-                P[j][2 * i2 + i] = dec == 0.f ? 0.f : P[j][2 * i2 + i] * dec;
-                s_a[t * kFA + s] = s < t && dec != 0.f ? be * (m * dec) : 0.f;
+                for (int i = 3; i >= 0; --i) {
+                    const float z = x * above;
+                    x = part * 32 + j * 4 + i == t ? first : z;
+                    above = as[i];
+                    f[i] = (is_p ? x : z) * __uint_as_float(y[j * 4 + i]);     // A: zero on the diagonal
+                }
+                if (is_p) {
+                    split_bf16(f[0], f[1], hi[part][2 * j], lo[part][2 * j]);
+                    split_bf16(f[2], f[3], hi[part][2 * j + 1], lo[part][2 * j + 1]);
+                } else {
+                    *reinterpret_cast<float4*>(s_a + t * kFA + part * 32 + j * 4) = make_float4(f[0], f[1], f[2], f[3]);
+                }
             }
         }
+        if (is_p) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                tmem_st16(lanes + DPrep::tP + part * 16, hi[part]);
+                tmem_st16(lanes + DPrep::tP + 32 + part * 16, lo[part]);
+            }
+            tmem_wait_st();
+        }
     }
-    if (tid < C) {
-        // gamma_t and gamma_C / gamma_t
-        const int I = tid >> 4;
-        const float all0 = s_pre[15], all3 = s_pre[63];
-        const float before = I == 0 ? 1.f : I == 1 ? all0 : I == 2 ? all0 * all1 : all0 * all1 * all2;
-        const float after = I == 3 ? 1.f : I == 2 ? all3 : I == 1 ? all2 * all3 : all1 * all2 * all3;
-        s_ga[tid] = before * s_pre[tid];
-        s_w[tid] = after * s_post[tid];
-    }
+    tc_fence_before();
     __syncthreads();
+    if (fine) {
     // ---- T = (I + A)^-1, lower triangle: the four 16 x 16 diagonal blocks by
     // substitution (a lane a column), then pairs of blocks, then halves: the
     // block below the diagonal is -T22 (A21 T11).  The unused upper blocks of
@@ -389,51 +386,62 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(const Ch
         reinterpret_cast<float*>(img + DRec::gam)[tid] = s_ga[tid];
         reinterpret_cast<float*>(img + DRec::w)[tid] = s_w[tid];
     }
-    __syncthreads();
-    // ---- G = P T', over the k steps and column tiles the triangles leave
-    float (&G)[8][4] = M;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) G[j][i] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-        if (ks > warp) break;
-        uint32_t ph[4], pl[4];
-        split_bf16(P[2 * ks][0], P[2 * ks][1], ph[0], pl[0]);
-        split_bf16(P[2 * ks][2], P[2 * ks][3], ph[1], pl[1]);
-        split_bf16(P[2 * ks + 1][0], P[2 * ks + 1][1], ph[2], pl[2]);
-        split_bf16(P[2 * ks + 1][2], P[2 * ks + 1][3], ph[3], pl[3]);
-#pragma unroll
-        for (int j = 0; j <= ks; ++j) {
-            uint32_t bh[4], bl[4];
-            const uint32_t at = base + DPrep::img + swz(ks * 16 + (lane & 15), j * 32 + (lane >> 4) * 16);
-            ldsm4t(bh, at + DRec::th);
-            ldsm4t(bl, at + DRec::tl);
-            mma16816(G[2 * j], ph, bh[0], bh[1]);
-            mma16816(G[2 * j + 1], ph, bh[2], bh[3]);
-            mma16816(G[2 * j], pl, bh[0], bh[1]);
-            mma16816(G[2 * j + 1], pl, bh[2], bh[3]);
-            mma16816(G[2 * j], ph, bl[0], bl[1]);
-            mma16816(G[2 * j + 1], ph, bl[2], bl[3]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t hi, lo;
-            split_bf16(G[j][2 * i], G[j][2 * i + 1], hi, lo);
-            const uint32_t at = swz(r0 + g + 8 * i, (8 * j + c2) * 2);
-            *reinterpret_cast<uint32_t*>(img + DRec::gh + at) = hi;
-            *reinterpret_cast<uint32_t*>(img + DRec::gl + at) = lo;
-        }
     fence_proxy_async_smem();
     __syncthreads();
-    if (tid == 0) {
-        bulk_s2g(ca.records + ((size_t)blk * a.H + h) * DRec::bytes, smem_u32(img), DRec::bytes);
-        bulk_commit();
-        bulk_wait_read<0>();
+    // ---- G = P T': hi * hi, lo * hi, hi * lo (rows 64..127 of M are not used)
+    if (warp == 0) {
+        tc_fence_after();
+        if (elect_one()) {
+            constexpr uint32_t id = mma_idesc(128, 64, false, true);
+#pragma unroll
+            for (int ks = 0; ks < 12; ++ks)
+                mma_ts(tm + DPrep::tG, tm + DPrep::tP + 8 * (ks & 7),
+                       desc_mn_major(base + DPrep::img + (ks < 8 ? DRec::th : DRec::tl) + (ks & 3) * 2048, kMat), id,
+                       ks > 0);
+            tc_commit(bar_mma);
+        }
+    }
+    if (warp < 2 && __all_sync(0xffffffffu, bounded_wait(bar_mma, 1, a.wait_ns, &s_abort, false))) {
+        tc_fence_after();
+        const int t = warp * 32 + lane;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            uint32_t y[32];
+            tmem_ld32(lanes + DPrep::tG + part * 32, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 hi, lo;
+                split_bf16(__uint_as_float(y[8 * j]), __uint_as_float(y[8 * j + 1]), hi.x, lo.x);
+                split_bf16(__uint_as_float(y[8 * j + 2]), __uint_as_float(y[8 * j + 3]), hi.y, lo.y);
+                split_bf16(__uint_as_float(y[8 * j + 4]), __uint_as_float(y[8 * j + 5]), hi.z, lo.z);
+                split_bf16(__uint_as_float(y[8 * j + 6]), __uint_as_float(y[8 * j + 7]), hi.w, lo.w);
+                const uint32_t at = swz(t, part * 64 + j * 16);
+                *reinterpret_cast<uint4*>(img + DRec::gh + at) = hi;
+                *reinterpret_cast<uint4*>(img + DRec::gl + at) = lo;
+            }
+        }
+    }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        if (s_abort) {
+            // nothing in flight when TMEM and shared memory are given back
+            mbar_wait_bounded(bar_in, 0, a.wait_ns);
+            if (elect_one()) tc_commit(bar_mma);
+            for (int i = 0; i < 2; ++i) mbar_wait_bounded(bar_mma, i, a.wait_ns);
+        }
+        tmem_free(tm, DPrep::cols);
+        if (s_abort) {
+            if (lane == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
+        } else if (elect_one()) {
+            bulk_s2g(ca.records + ((size_t)blk * a.H + h) * DRec::bytes, smem_u32(sm + DPrep::img), DRec::bytes);
+            bulk_commit();
+            bulk_wait_read<0>();
+        }
     }
 }
 
@@ -585,7 +593,6 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             }
             tmem_wait_st();
             arrive(X::CS + part / 2);
-            //@CK(1)
             // ---- R = V - diag(gamma) K S
             if (!(ok = wait_group(warp == 0, X::Full + c % X::kStages, (c / X::kStages) & 1, 4, X::kWarps * 32)))
                 break;
@@ -599,7 +606,6 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             }
             uint32_t x[16], h8[8], l8[8];
             if (!(ok = wait_group(warp == 0, X::BK, ph, 4, X::kWarps * 32))) break;
-            //@CK(2)
             tc_fence_after();
             tmem_ld16(lanes + X::KQ + part * 16, x);
             tmem_wait_ld();
@@ -612,10 +618,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             tmem_st8(lanes + X::Rh + 32 + part * 8, l8);
             tmem_wait_st();
             arrive(X::CR);
-            //@CK(3)
             // ---- diag(w) U as a pair
             if (!(ok = wait_group(warp == 0, X::BU, ph, 4, X::kWarps * 32))) break;
-            //@CK(4)
             tc_fence_after();
             tmem_ld16(lanes + X::UO + part * 16, x);
             tmem_wait_ld();
@@ -628,11 +632,9 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             const float gc = gam[C - 1];
             tmem_wait_st();
             arrive(X::CU);
-            //@CK(5)
             // ---- S <- gamma_C S + the block's part
             if (!(ok = wait_group(quad + (part & 1) == 0, X::BS + part / 2, ph, 2 + part / 2, X::kWarps * 16)))
                 break;
-            //@CK(6)
             tc_fence_after();
             uint32_t y[32];
             tmem_ld32(lanes + X::dS + part * 32, y);
@@ -1350,7 +1352,7 @@ cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
     }
     ca.first_block = reinterpret_cast<int32_t*>(a.work);
     ca.records = a.work + first_block_bytes(a.n);
-    delta_prepare_kernel<<<a.max_blocks * a.H, kPrepThreads, DPrep::bytes, s>>>(ca);
+    delta_prepare_kernel<<<a.max_blocks * a.H, kPrepThreads, DPrep::bytes, s>>>(ca, mq, mk);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     delta_chain_kernel<<<a.n * a.H, DChain::threads, DChain::bytes, s>>>(ca, mq, mk, mv);
     return cudaGetLastError();
