@@ -493,11 +493,10 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int req = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const int end = min(max(__ldg(a.cu_seqlens + req + 1), 0), a.max_tokens);
-    const int start = min(max(__ldg(a.cu_seqlens + req), 0), end);
-    const int len = end - start;
+    const int cu0 = __ldg(a.cu_seqlens + req), cu1 = __ldg(a.cu_seqlens + req + 1);
+    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req), block0 = ca.first_block[req];
+    const int end = min(max(cu1, 0), a.max_tokens), start = min(max(cu0, 0), end), len = end - start;
     if (len == 0) return;
-    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)start * a.H + h) * D;
     if (slot < 0 || slot >= a.n_slots) {
         if (slot >= a.n_slots && tid == 0 && h == 0) atomicOr(a.status, DAMP_EFLAG_SLOT_RANGE);
@@ -508,25 +507,56 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     }
     const int nc = (len + C - 1) / C;
     // a plan's first_block + nc always fits; anything else is kept inside the workspace
-    const int fb = min(max(ca.first_block[req], 0), max(a.max_blocks - nc, 0));
+    const int fb = min(max(block0, 0), max(a.max_blocks - nc, 0));
     auto bar = [&](int i) { return base + X::bar + 8 * i; };
 
-    if (tid == 0) {
-        for (int i = 0; i < X::kStages; ++i) {
-            mbar_init(bar(X::Full + i), 1);
-            mbar_init(bar(X::Empty + i), X::kWarps / 2 + X::kOut);
+    constexpr int wLoad = X::kWarps + X::kOut, wMma = wLoad + 1;
+    auto load = [&](int c) {                           // one lane: block c into its stage
+        const int hq = h / (a.H / a.H_qk), t = start + c * C;
+        const uint32_t st = base + c % X::kStages * X::stage, f = bar(X::Full + c % X::kStages);
+        mbar_arrive_expect_tx(f, 3 * kTile + DRec::bytes);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            tma_load_3d(st + X::kq + half * kTile, &mk, half * 64, hq, t, f);
+            tma_load_3d(st + X::kq + half * kTile + kHalf, &mq, half * 64, hq, t, f);
+            tma_load_3d(st + X::v + half * kHalf, &mv, half * 64, h, t, f);
         }
-        for (int i = X::BK; i < X::CS; ++i) mbar_init(bar(i), 1);
-        mbar_init(bar(X::CS), X::kWarps / 2);
-        mbar_init(bar(X::CS + 1), X::kWarps / 2);
-        mbar_init(bar(X::CR), X::kWarps);
-        mbar_init(bar(X::CU), X::kWarps);
-        mbar_init(bar(X::CO), X::kOut);
-        mbar_init(bar(X::Drain), 1);
-        fence_mbar_init();
-        s_abort = 0;
+        bulk_g2s(st + X::rec, ca.records + ((size_t)(fb + c) * a.H + h) * DRec::bytes, DRec::bytes, f);
+        // a stage is not free early enough to cover DRAM's latency: the next blocks come to L2
+        // ahead of their turn
+        const int n = c + X::kStages, tn = start + n * C;
+        if (n < nc) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                tma_prefetch_3d(&mk, half * 64, hq, tn);
+                tma_prefetch_3d(&mq, half * 64, hq, tn);
+                tma_prefetch_3d(&mv, half * 64, h, tn);
+            }
+            bulk_prefetch(ca.records + ((size_t)(fb + n) * a.H + h) * DRec::bytes, DRec::bytes);
+        }
+    };
+    if (warp == wLoad) {
+        if (elect_one()) {
+            for (int i = 0; i < X::kStages; ++i) {
+                mbar_init(bar(X::Full + i), 1);
+                mbar_init(bar(X::Empty + i), X::kWarps / 2 + X::kOut);
+            }
+            for (int i = X::BK; i < X::CS; ++i) mbar_init(bar(i), 1);
+            mbar_init(bar(X::CS), X::kWarps / 2);
+            mbar_init(bar(X::CS + 1), X::kWarps / 2);
+            mbar_init(bar(X::CR), X::kWarps);
+            mbar_init(bar(X::CU), X::kWarps);
+            mbar_init(bar(X::CO), X::kOut);
+            mbar_init(bar(X::Drain), 1);
+            fence_mbar_init();
+            s_abort = 0;
+            // the first blocks are on their way before the rest of the CTA is ready
+            for (int c = 0; c < min(nc, X::kStages); ++c) load(c);
+        }
+        __syncwarp();
+    } else if (warp == wMma) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
     }
-    if (warp == X::kWarps + X::kOut) tmem_alloc(smem_u32(&s_tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -693,38 +723,12 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             }
             bar_sync(1, X::kOut * 32);
         }
-    } else if (warp == X::kWarps + X::kOut) {
+    } else if (warp == wLoad) {
         // ---------------------------------------------------------- loads
-        const int hq = h / (a.H / a.H_qk);
-        int issued = 0;
-        for (int c = 0; c < nc; ++c) {
-            const int s = c % X::kStages;
-            if (c >= X::kStages && !wait_all(X::Empty + s, (c / X::kStages - 1) & 1)) break;
-            const uint32_t st = base + s * X::stage, f = bar(X::Full + s);
-            const int t = start + c * C;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(f, 3 * kTile + DRec::bytes);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    tma_load_3d(st + X::kq + half * kTile, &mk, half * 64, hq, t, f);
-                    tma_load_3d(st + X::kq + half * kTile + kHalf, &mq, half * 64, hq, t, f);
-                    tma_load_3d(st + X::v + half * kHalf, &mv, half * 64, h, t, f);
-                }
-                bulk_g2s(st + X::rec, ca.records + ((size_t)(fb + c) * a.H + h) * DRec::bytes,
-                         DRec::bytes, f);
-                // a stage is not free early enough to cover DRAM's latency: the next blocks come
-                // to L2 ahead of their turn
-                for (int n = c == 0 ? 1 : X::kStages; n <= X::kStages && c + n < nc; ++n) {
-                    const int tn = t + n * C;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        tma_prefetch_3d(&mk, half * 64, hq, tn);
-                        tma_prefetch_3d(&mq, half * 64, hq, tn);
-                        tma_prefetch_3d(&mv, half * 64, h, tn);
-                    }
-                    bulk_prefetch(ca.records + ((size_t)(fb + c + n) * a.H + h) * DRec::bytes, DRec::bytes);
-                }
-            }
+        int issued = min(nc, X::kStages);
+        for (int c = X::kStages; c < nc; ++c) {
+            if (!wait_all(X::Empty + c % X::kStages, (c / X::kStages - 1) & 1)) break;
+            if (elect_one()) load(c);
             issued = c + 1;
         }
         // copies in flight end before the CTA does
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     tc_fence_before();
     __syncthreads();
     if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
-    if (warp == X::kWarps + X::kOut) {
+    if (warp == wMma) {
         tc_fence_after();
         tmem_free(tm, 512);
     }
@@ -864,14 +868,14 @@ __global__ void __launch_bounds__(EChain::threads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int seg = blockIdx.x % sa.segs, unit = blockIdx.x / sa.segs;
     const int req = unit / a.H, h = unit % a.H;
-    const int end = min(max(__ldg(a.cu_seqlens + req + 1), 0), a.max_tokens);
-    const int first = min(max(__ldg(a.cu_seqlens + req), 0), end);
+    const int cu0 = __ldg(a.cu_seqlens + req), cu1 = __ldg(a.cu_seqlens + req + 1);
+    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
+    const int end = min(max(cu1, 0), a.max_tokens), first = min(max(cu0, 0), end);
     if (first == end) return;
     const int blocks = (end - first + C - 1) / C, per = (blocks + sa.segs - 1) / sa.segs;
     if (seg * per >= blocks || (SUM && (seg + 1) * per >= blocks)) return;   // nothing, or no one to hand on to
     const bool last = (seg + 1) * per >= blocks;
     const int start = first + seg * per * C, len = min(end - start, per * C), nc = (len + C - 1) / C;
-    const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)start * a.H + h) * D;
     if (slot < 0 || slot >= a.n_slots) {
         if (SUM) return;
@@ -883,25 +887,42 @@ __global__ void __launch_bounds__(EChain::threads, 1)
     }
     auto bar = [&](int i) { return base + X::bar + 8 * i; };
 
-    if (tid == 0) {
-        for (int i = 0; i < X::kStages; ++i) {
-            mbar_init(bar(X::Full + i), 2);
-            mbar_init(bar(X::Empty + i), 1 + X::kForm);
+    auto load = [&](int c) {                           // one lane: block c into its stage
+        const int hq = h / (a.H / a.H_qk), t = start + c * C;
+        const uint32_t st = base + c % X::kStages * X::stage, f = bar(X::Full + c % X::kStages);
+        mbar_arrive_expect_tx(f, (SUM ? 2 : 3) * kTile);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            tma_load_3d(st + X::v + half * kHalf, &mv, half * 64, h, t, f);
+            tma_load_3d(st + X::k + half * kHalf, &mk, half * 64, hq, t, f);
+            if (!SUM) tma_load_3d(st + X::q + half * kHalf, &mq, half * 64, hq, t, f);
         }
-        for (int i = X::BD; i < X::CV; ++i) mbar_init(bar(i), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(X::CV + i), X::kForm);
-            mbar_init(bar(X::CP + i), X::kForm);
+    };
+    if (warp == X::wLoad) {
+        if (elect_one()) {
+            for (int i = 0; i < X::kStages; ++i) {
+                mbar_init(bar(X::Full + i), 2);
+                mbar_init(bar(X::Empty + i), 1 + X::kForm);
+            }
+            for (int i = X::BD; i < X::CV; ++i) mbar_init(bar(i), 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar(X::CV + i), X::kForm);
+                mbar_init(bar(X::CP + i), X::kForm);
+            }
+            mbar_init(bar(X::CD), X::kWarps);
+            mbar_init(bar(X::CP0), X::kForm);
+            mbar_init(bar(X::CS), X::kWarps);
+            mbar_init(bar(X::CO), X::kOut);
+            mbar_init(bar(X::Drain), 1);
+            fence_mbar_init();
+            s_abort = 0;
+            // the first blocks are on their way before the rest of the CTA is ready
+            for (int c = 0; c < min(nc, X::kStages); ++c) load(c);
         }
-        mbar_init(bar(X::CD), X::kWarps);
-        mbar_init(bar(X::CP0), X::kForm);
-        mbar_init(bar(X::CS), X::kWarps);
-        mbar_init(bar(X::CO), X::kOut);
-        mbar_init(bar(X::Drain), 1);
-        fence_mbar_init();
-        s_abort = 0;
+        __syncwarp();
+    } else if (warp == X::wMma) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
     }
-    if (warp == X::wLoad) tmem_alloc(smem_u32(&s_tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1136,27 +1157,18 @@ __global__ void __launch_bounds__(EChain::threads, 1)
         }
     } else if (warp == X::wLoad) {
         // ---------------------------------------------------------- loads
-        const int hq = h / (a.H / a.H_qk);
-        int issued = 0;
+        int issued = min(nc, X::kStages);
         auto alpha_of = [&](int t) {
             return t < len ? __ldg(a.alpha + (size_t)(start + t) * a.H + h) : 1.f;
         };
         float a0 = alpha_of(2 * lane), a1 = alpha_of(2 * lane + 1);    // of this lane's two tokens
         for (int c = 0; c < nc; ++c) {
-            const int s = c % X::kStages;
-            if (c >= X::kStages && !wait_all(X::Empty + s, (c / X::kStages - 1) & 1)) break;
-            const uint32_t st = base + s * X::stage, f = bar(X::Full + s);
-            const int t = start + c * C;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(f, (SUM ? 2 : 3) * kTile);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    tma_load_3d(st + X::v + half * kHalf, &mv, half * 64, h, t, f);
-                    tma_load_3d(st + X::k + half * kHalf, &mk, half * 64, hq, t, f);
-                    if (!SUM) tma_load_3d(st + X::q + half * kHalf, &mq, half * 64, hq, t, f);
-                }
+            const uint32_t f = bar(X::Full + c % X::kStages);
+            if (c >= X::kStages) {
+                if (!wait_all(X::Empty + c % X::kStages, (c / X::kStages - 1) & 1)) break;
+                if (elect_one()) load(c);
+                issued = c + 1;
             }
-            issued = c + 1;
             // products of the decays up to each token, and behind it
             float up = a0 * a1, down = up;
 #pragma unroll
@@ -1259,7 +1271,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
     tc_fence_before();
     __syncthreads();
     if (s_abort && tid == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
-    if (warp == X::wLoad) {
+    if (warp == X::wMma) {
         tc_fence_after();
         tmem_free(tm, 512);
     }
