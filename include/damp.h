@@ -301,7 +301,7 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
  *           bf16 or float32 (in_dtype), heads and channels dense; *_stride =
  *           elements between token rows (views of one projection's output are
  *           fine), a multiple of 16 bytes.
- *   alpha : device float32 [max_tokens][H], >= 0 (0 forgets the state)
+ *   alpha : device float32 [max_tokens][H] (0 forgets the state)
  *   beta  : device float32 [max_tokens][H] (DAMP_RULE_DELTA; NULL for DECAY)
  *   out   : device [max_tokens][H][d_v], dense, the type of q.  Rows of
  *           requests without a slot are zeroed; rows behind the last request
@@ -309,13 +309,19 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
  *   workspace : device, damp_prefill_workspace bytes, 256-byte aligned; not
  *           shared by calls that may run at the same time.  NULL allowed when
  *           that is 0.
- * A request with load_slot >= 0 continues from that slot's state, another
- * starts from zeros; a slot the plan does not store to keeps its bytes.  A
- * store_slot >= n_slots sets DAMP_EFLAG_SLOT_RANGE (rows zeroed).  States are
- * FP32 inside the call: a quantized pool's are dequantized before it and
- * quantized once after it (damp_pool_unpack / damp_pool_pack).
- * The readout is computed from FP32 states and rounded once to the output's
- * type.
+ * A request with load_slot >= 0 (its own store_slot) continues from that slot's
+ * state, another starts from zeros; a slot the plan does not store to keeps its
+ * bytes.  A store_slot >= n_slots sets DAMP_EFLAG_SLOT_RANGE (rows zeroed).
+ * States are FP32 inside the call: a quantized pool's are dequantized before it
+ * and quantized once after it (damp_pool_unpack / damp_pool_pack).
+ * Inputs are finite; a request's values reach no other request's results.
+ * Arithmetic: FP32, token by token, and the readout rounded once; bf16 layers
+ * with d_k = d_v = 128 run in blocks of 64 tokens on the tensor cores, where
+ * every FP32 operand enters as two bf16 values (2^-17 of it are lost): states
+ * and readouts before their rounding are within about 1e-5 of the recurrence in
+ * 64 bits, relative to their norm.  The same call gives the same bits.
+ * A wait inside the call that runs out sets DAMP_EFLAG_TIMEOUT; the results of
+ * that call are not valid.
  */
 int damp_prefill_workspace(const damp_pool* pool, int rule, int n, int max_tokens, int in_dtype,
                            size_t* bytes);
@@ -328,8 +334,8 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
 
 /*
  * Test hooks of the failure path (for tests of the library; not for serving).
- *   wait_limit_ns : bound of every internal pipeline wait of the decode step;
- *                   0 restores the default (2 s).  A wait that runs out sets
+ *   wait_limit_ns : bound of every internal pipeline wait of the decode step
+ *                   and of damp_prefill; 0 restores the default (2 s).  A wait that runs out sets
  *                   DAMP_EFLAG_TIMEOUT in the pool's status word; the kernel
  *                   then waits (bounded) for its copies in flight and returns,
  *                   so the CUDA context stays usable.
@@ -337,6 +343,10 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
  *                   step leaves the loads of its first work item unissued, so
  *                   the wait for them runs out; no unit of the call is
  *                   updated or stored and the out rows are left as they were.
+ *                   damp_prefill's tensor-core kernels leave the first loads of
+ *                   every CTA unissued likewise: a request's state is left as
+ *                   it was (quantized pools: as packed again from what the call
+ *                   unpacked, zeros for a request without a past).
  * Process-wide, for the launches enqueued after the call.
  */
 #define DAMP_HOOK_HOLD_FIRST_ITEM 1u

@@ -703,10 +703,10 @@ def damp_calib_select_budget_static(H: int, d_k: int, budget: int, acc: torch.Te
 # ---------------------------------------------------------------- convenience
 
 class BatchPlan:
-    """Buffers of a ragged batch's index arrays (damp_batch_plan) for up to
-    ``n`` requests and ``max_tokens`` token rows.  ``build`` fills them on the
-    device; a captured ``build`` reads the lengths its tensors hold at
-    replay."""
+    """Buffers of a ragged batch's index arrays (damp_batch_plan) for ``n``
+    requests (a length of 0 for one that has no tokens now) and up to
+    ``max_tokens`` token rows.  ``build`` fills them on the device; a captured
+    ``build`` reads the lengths its tensors hold at replay."""
 
     def __init__(self, n: int, max_tokens: int, n_slots: int, device="cuda", token_maps=True):
         self.n, self.max_tokens, self.n_slots = n, max_tokens, n_slots
@@ -716,13 +716,21 @@ class BatchPlan:
         self.block_table, self.totals = e(self.max_blocks, 4), e(4)
         self.token_slot, self.token_pos = (e(max_tokens), e(max_tokens)) if token_maps \
             else (None, None)
+        # the buffers stay this object's own: their addresses are looked up once
+        self._out = [None if t is None else t.data_ptr()
+                     for t in (self.cu_seqlens, self.load_slot, self.store_slot, self.block_table,
+                               self.token_slot, self.token_pos, self.totals)]
 
     def build(self, lengths: torch.Tensor, slot_idx: torch.Tensor, past=None, stream=None):
         """Index arrays of requests with ``lengths`` tokens each, ``past``
         tokens already in their states, and state slots ``slot_idx``."""
-        damp_batch_plan(lengths, slot_idx, past, self.n_slots, self.max_tokens, self.cu_seqlens,
-                        self.load_slot, self.store_slot, self.block_table, self.token_slot,
-                        self.token_pos, self.totals, stream)
+        n, i32, dev = self.n, torch.int32, self.cu_seqlens.device
+        ptr = (_want(lengths, "lengths", (n,), i32, dev),
+               None if past is None else _want(past, "past", (n,), i32, dev),
+               _want(slot_idx, "slot_idx", (n,), i32, dev))
+        with _on_device(dev):
+            _check(_lib.damp_batch_plan(n, *ptr, self.n_slots, self.max_tokens, *self._out,
+                                        _launch_stream(stream, dev)), "damp_batch_plan")
         return self
 
 
@@ -814,6 +822,8 @@ class DampPool:
                 stream=None) -> torch.Tensor:
         """The prompts of a built BatchPlan through one layer (damp_prefill);
         returns ``out`` (allocated, zero-filled, when None)."""
+        if isinstance(q, torch.Tensor) and q.dim() == 3 and q.shape[0] != plan.max_tokens:
+            raise ValueError(f"the plan is for {plan.max_tokens} token rows, got {q.shape[0]}")
         if plan.n_slots > self.n_slots:
             raise ValueError(f"the plan allows slots up to {plan.n_slots}, the pool has "
                              f"{self.n_slots}")

@@ -227,7 +227,6 @@ int create_common(int format, int n_slots, int H, int d_k, int d_v, int hp_rows,
         }
         cudaError_t e = cudaMemcpy(dev_buf, hdr.data(), hdr.size(), cudaMemcpyHostToDevice);
         if (e == cudaSuccess) e = damp::prepare_decode(d);
-        if (e == cudaSuccess) e = damp::prepare_plan();
         if (e == cudaSuccess && d.d_k == 128 && d.d_v == 128) e = damp::prepare_prefill();
         if (e != cudaSuccess) {
             delete[] p->d.host_masks;
@@ -553,6 +552,8 @@ int prefill_space(const damp_pool* pool, int rule, int n, int max_tokens, int in
     w->chunked = damp::prefill_chunk_fits(d.d_k, d.d_v, in_dtype == DAMP_DTYPE_BF16);
     int blocks = 0;
     damp_plan_blocks(n, max_tokens, &blocks);
+    // one CTA per (block, head) and per (request, head, segment)
+    if ((long long)(blocks > n ? blocks : n) * d.H > 0x7fffffffll) return DAMP_ERR_UNSUPPORTED;
     w->total = w->states + (w->chunked ? damp::prefill_chunk_bytes(n, d.H, max_tokens, blocks,
                                                                    rule == DAMP_RULE_DELTA)
                                        : 0);
@@ -631,6 +632,7 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
     a.bf16 = in_dtype == DAMP_DTYPE_BF16;
     const unsigned long long wait = g_wait_ns.load(std::memory_order_relaxed);
     a.wait_ns = wait ? wait : damp::kDefaultWaitNs;
+    a.hooks = g_hooks.load(std::memory_order_relaxed);
     a.work = static_cast<uint8_t*>(workspace) + w.states;
     damp_plan_blocks(n, max_tokens, &a.max_blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -57,6 +57,12 @@ struct PoolDesc {
     size_t head_off;           // byte offset of the block table in the header
 };
 
+// Test hook of the failure path: the refill side of every CTA never issues its
+// first item (no copy, no arrival), so the consumers' bounded wait for it runs
+// out and the kernel takes its abort path.
+constexpr uint32_t kHookHoldFirstItem = 1u;
+constexpr unsigned long long kDefaultWaitNs = 2000000000ull;   // 2 s
+
 // Arguments of the decode-step kernel.
 struct StepArgs {
     uint8_t* blocks;           // first block
@@ -86,12 +92,6 @@ struct StepArgs {
     uint32_t hooks;            // test hooks (kHookHoldFirstItem)
     int validate;              // 1: units with a non-finite input are skipped and flagged
 };
-
-// Test hook of the failure path: the refill side of every CTA never issues its
-// first item (no copy, no arrival), so the consumers' bounded wait for it runs
-// out and the kernel takes its abort path.
-constexpr uint32_t kHookHoldFirstItem = 1u;
-constexpr unsigned long long kDefaultWaitNs = 2000000000ull;   // 2 s
 
 // Arguments of the pack / unpack kernels.
 struct CodecArgs {
@@ -159,11 +159,11 @@ struct PrefillArgs {
     int delta;                 // 1: gated delta rule, 0: decay rule
     int bf16;
     unsigned long long wait_ns;
+    uint32_t hooks;            // test hooks (kHookHoldFirstItem)
     uint8_t* work;             // chunk kernels' workspace
     int max_blocks;
 };
 
-cudaError_t prepare_plan();
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
 // One token of the decay rule on the pool's blocks, every shape and format
 // (damp_decay_step.cu); a.beta is not read.

@@ -185,11 +185,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 
 }  // namespace
 
-cudaError_t prepare_plan() {
-    return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                DAMP_PLAN_MAX_REQUESTS * 8);
-}
-
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -197,7 +192,9 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     const size_t smem = (size_t)a.n * 8;
-    if (smem > 48 * 1024 && (e = prepare_plan()) != cudaSuccess) return e;
+    if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      DAMP_PLAN_MAX_REQUESTS * 8)) != cudaSuccess)
+        return e;
     const long long rows = std::max((long long)a.max_tokens, (long long)a.max_blocks);
     const int grid = (int)std::max(1ll, std::min((long long)sms, (rows + kRowsPerCta - 1) / kRowsPerCta));
     plan_kernel<<<grid, kPlanThreads, smem, stream>>>(a);

@@ -155,11 +155,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             fence_mbar_init();
             s_abort = 0;
             const int hq = h / (a.H / a.H_qk);
-            mbar_arrive_expect_tx(bar_in, 2 * kTile);
+            if (!(a.hooks & kHookHoldFirstItem)) {
+                mbar_arrive_expect_tx(bar_in, 2 * kTile);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                tma_load_3d(base + DPrep::qk + half * kTile, &mq, half * 64, hq, t0, bar_in);
-                tma_load_3d(base + DPrep::qk + half * kTile + kHalf, &mk, half * 64, hq, t0, bar_in);
+                for (int half = 0; half < 2; ++half) {
+                    tma_load_3d(base + DPrep::qk + half * kTile, &mq, half * 64, hq, t0, bar_in);
+                    tma_load_3d(base + DPrep::qk + half * kTile + kHalf, &mk, half * 64, hq, t0, bar_in);
+                }
             }
         }
         __syncwarp();
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             fence_mbar_init();
             s_abort = 0;
             // the first blocks are on their way before the rest of the CTA is ready
-            for (int c = 0; c < min(nc, X::kStages); ++c) load(c);
+            for (int c = a.hooks & kHookHoldFirstItem ? 1 : 0; c < min(nc, X::kStages); ++c) load(c);
         }
         __syncwarp();
     } else if (warp == wMma) {
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             fence_mbar_init();
             s_abort = 0;
             // the first blocks are on their way before the rest of the CTA is ready
-            for (int c = 0; c < min(nc, X::kStages); ++c) load(c);
+            for (int c = a.hooks & kHookHoldFirstItem ? 1 : 0; c < min(nc, X::kStages); ++c) load(c);
         }
         __syncwarp();
     } else if (warp == X::wMma) {
@@ -1021,15 +1023,17 @@ __global__ void __launch_bounds__(EChain::threads, 1)
                 for (int i = 0; i < 32; ++i) to[(size_t)i * D] = S[i];
             }
         }
-    } else if (warp < X::wOut) {
+    } else if (warp < (SUM ? X::wLoad : X::wOut)) {
         // ---------------------------------------------------------- operands
-        constexpr int kId = 2, kN = X::kForm * 32;
-        const int ft = tid - X::kWarps * 32, c2 = (lane & 3) * 2;
+        // (in a first pass the readout's warps have every other block's)
+        constexpr int kN = X::kForm * 32;
+        const int group = (warp - X::kWarps) / X::kForm, kId = 2 + group, lead = X::kWarps + group * X::kForm;
+        const int ft = tid - lead * 32, c2 = (lane & 3) * 2;
         // diag(w) V of block c as a pair in TMEM
         auto form_v = [&](int c) -> bool {
             const uint32_t st = base + c % X::kStages * X::stage, buf = c & 1;
             const int live = min(C, len - c * C);
-            if (!wait_group(warp == X::kWarps, X::Full + c % X::kStages, (c / X::kStages) & 1, kId, kN)) return false;
+            if (!wait_group(warp == lead, X::Full + c % X::kStages, (c / X::kStages) & 1, kId, kN)) return false;
             if (live < C) {
                 // rows behind the end hold another request's keys and values: they must not
                 // enter the sums over tokens
@@ -1041,7 +1045,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
                 }
             }
             // the block before last has used this pair up
-            if (!wait_group(c >= 2 && warp == X::kWarps, X::BD + buf, ((c >> 1) - 1) & 1, kId, kN)) return false;
+            if (!wait_group(c >= 2 && warp == lead, X::BD + buf, ((c >> 1) - 1) & 1, kId, kN)) return false;
             const float* w = ring(c) + 2 * C;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {   // 16 value columns (TMEM lanes) each, transposed by ldmatrix
@@ -1071,13 +1075,18 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             if (lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
             return true;
         };
-        bool ok = form_v(0) && (nc < 2 || form_v(1));
+        bool ok = true;
+        if (SUM) {
+            for (int c = group; c < nc && ok; c += 2) ok = form_v(c);
+        } else {
+            ok = form_v(0) && (nc < 2 || form_v(1));
+        }
         // this thread's token and its 32 columns of P (TMEM lanes 0..63: 0..31, 64..127: 32..63)
         const int t = (quad & 1) * 32 + lane, s0 = (quad >> 1) * 32;
-        for (int c = 0; c < nc && ok; ++c) {
-            if (!SUM) {
+        for (int c = 0; c < (SUM ? 0 : nc) && ok; ++c) {
+            {
                 uint8_t* pm = sm + X::p + (c & 1) * 2 * kMat;
-                if (!(ok = wait_group(warp == X::kWarps, X::BP, c & 1, kId, kN))) break;
+                if (!(ok = wait_group(warp == lead, X::BP, c & 1, kId, kN))) break;
                 tc_fence_after();
                 uint32_t y[32];
                 tmem_ld32(lanes + X::dS + s0, y);
@@ -1118,7 +1127,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
         // ---------------------------------------------------------- readout
         const int wt = tid - X::wOut * 32;
         uint8_t* so = sm + X::out;
-        for (int c = 0; c < (SUM ? 0 : nc); ++c) {
+        for (int c = 0; c < nc; ++c) {
             const float* gam = ring(c) + C;
             if (!wait_group(warp == X::wOut, X::BO + (c & 1), (c >> 1) & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
@@ -1299,10 +1308,10 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int heads, long long rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Segments of a request for the decay rule: enough for two thirds of the SMs
-// or more to have one, none shorter (on average) than 4 blocks; a batch whose
-// (request, head) pairs fill the SMs stays whole (the first pass reads K and V
-// once more: +50 % bytes).  TODO measured
+// Segments of a request for the decay rule: as many as the SMs have room for,
+// none shorter (on average) than 4 blocks; a batch whose (request, head) pairs
+// take more than half of the SMs stays whole (the first pass reads K and V once
+// more).  One prompt of 4096 tokens x 32 heads: 81 us in 4 segments, 187 whole.
 int decay_segments(int n, int H, int max_tokens, int sms) {
     const long long chains = (long long)n * H;
     if (chains * 2 > sms) return 1;
@@ -1314,26 +1323,28 @@ size_t first_block_bytes(int n) { return ((size_t)n * 4 + 255) / 256 * 256; }
 
 }  // namespace
 
+// The driver's encoder and the kernels' attributes, once per device (the
+// current one).
 cudaError_t prepare_prefill() {
+    static std::atomic<uint64_t> ready{0};             // a bit per device below 64
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (ready.load() >> dev & 1)) return cudaSuccess;
     if (!g_encode.load()) {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q);
+        e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q);
         if (e != cudaSuccess || q != cudaDriverEntryPointSuccess) return e != cudaSuccess ? e : cudaErrorNotSupported;
         g_encode.store(reinterpret_cast<EncodeTiled>(f));
     }
-    cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DPrep::bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 DChain::bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decay_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 EChain::bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decay_chain_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 EChain::bytes);
-    return e;
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if ((e = cudaFuncSetAttribute(delta_prepare_kernel, attr, DPrep::bytes)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(delta_chain_kernel, attr, DChain::bytes)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(decay_chain_kernel<false>, attr, EChain::bytes)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(decay_chain_kernel<true>, attr, EChain::bytes)) != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev);
+    return cudaSuccess;
 }
 
 bool prefill_chunk_fits(int d_k, int d_v, int bf16) { return bf16 && d_k == D && d_v == D; }
@@ -1346,7 +1357,8 @@ size_t prefill_chunk_bytes(int n, int H, int max_tokens, int max_blocks, int del
 
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
-    cudaError_t e = token_map(&mq, a.q, a.H_qk, a.max_tokens, a.q_stride);
+    cudaError_t e = prepare_prefill();
+    if (e == cudaSuccess) e = token_map(&mq, a.q, a.H_qk, a.max_tokens, a.q_stride);
     if (e == cudaSuccess) e = token_map(&mk, a.k, a.H_qk, a.max_tokens, a.k_stride);
     if (e == cudaSuccess) e = token_map(&mv, a.v, a.H, a.max_tokens, a.v_stride);
     if (e != cudaSuccess) return e;

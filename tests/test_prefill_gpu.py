@@ -276,3 +276,128 @@ def test_prompt_then_single_tokens(rule):
     pool.unpack(i32([1]), S1)
     assert ((S1[0].double() - S).flatten(1).norm(dim=1) <= tol).all()
     pool.close()
+
+
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_request_does_not_see_its_neighbours(rule, dtype, bad):
+    """Requests 1 and 3 and the rows behind the last hold NaN or infinities; blocks of the others
+    end inside the same 64-row tiles."""
+    H, d, lengths = 2, 128, [70, 5, 30, 90, 1, 64]
+    T = sum(lengths) + 80
+    x = inputs(torch.Generator().manual_seed(4), T, H, H, d, d, dtype)
+    at = np.concatenate([[0], np.cumsum(lengths)])
+
+    def run(x):
+        pool = D.DampPool("fp32", 6, H, d)
+        pool.slots().fill_(0)
+        plan = D.BatchPlan(6, T, 6).build(i32(lengths), i32([0, 1, 2, 3, 4, 5]))
+        o = pool.prefill(plan, x["q"], x["k"], x["v"], x["alpha"],
+                         x["beta"] if rule == "delta" else None, rule=rule)
+        s = pool.slots().clone()
+        pool.close()
+        return o, s
+
+    o0, s0 = run(x)
+    y = {k: v.clone() for k, v in x.items()}
+    for r in (1, 3, 6):
+        a, b = (at[r], at[r + 1]) if r < 6 else (at[6], T)
+        for c in ("q", "k", "v", "alpha", "beta"):
+            y[c][a:b] = bad
+    o1, s1 = run(y)
+    for r in (0, 2, 4, 5):
+        assert torch.equal(o0[at[r]:at[r + 1]], o1[at[r]:at[r + 1]]), r
+        assert torch.equal(s0[r], s1[r]), r
+
+
+@pytest.mark.parametrize("rule", RULES)
+def test_a_wait_that_runs_out_is_reported(rule):
+    H, d, T = 3, 128, 150
+    x = inputs(torch.Generator().manual_seed(4), T, H, H, d, d, BF)
+    pool = D.DampPool("fp32", 3, H, d)
+    pool.slots().fill_(0)
+    plan = D.BatchPlan(2, T, 3).build(i32([100, 50]), i32([2, 0]), i32([1, 1]))
+    args = (plan, x["q"], x["k"], x["v"], x["alpha"], x["beta"] if rule == "delta" else None)
+    want = pool.prefill(*args, rule=rule)
+    states = pool.slots().clone()
+    pool.slots().fill_(0)
+    try:
+        D.damp_set_test_hooks(wait_limit_ns=3_000_000, hooks=D.DAMP_HOOK_HOLD_FIRST_ITEM)
+        pool.prefill(*args, rule=rule)
+        assert pool.get_error(clear=True) == D.DAMP_EFLAG_TIMEOUT
+        assert not pool.slots().any()
+    finally:
+        D.damp_set_test_hooks()
+    assert torch.equal(pool.prefill(*args, rule=rule), want)      # the context is as good as before
+    assert torch.equal(pool.slots(), states)
+    assert pool.get_error() == 0
+    pool.close()
+
+
+@pytest.mark.parametrize("rule", RULES)
+def test_many_short_requests_and_few_heads(rule):
+    g = np.random.default_rng(1)
+    lengths = g.integers(0, 9, 200).tolist()
+    check(rule, lengths, H=1, Hqk=1, dk=128, dv=128, dtype=BF, past=g.integers(0, 2, 200).tolist())
+
+
+def test_segments_of_long_requests():
+    """The decay rule cuts requests into segments where few chains would leave SMs idle; ragged
+    lengths give empty and short segments, and the first and the last one share a slot."""
+    for lengths in ([2048, 300, 5, 0, 64], [4000], [257, 1, 1900]):
+        check("decay", lengths, H=1, Hqk=1, dk=128, dv=128, dtype=BF, past=[1] * len(lengths), spare=7)
+        check("decay", lengths, H=2, Hqk=1, dk=128, dv=128, dtype=BF, past=[0] * len(lengths))
+
+
+@pytest.mark.parametrize("rule", RULES)
+def test_two_calls_at_once(rule):
+    """Two layers on two streams at the same time, each with its own pool and workspace."""
+    H, d, T = 4, 128, 700
+    x = inputs(torch.Generator().manual_seed(8), T, H, H, d, d, BF)
+    plan = D.BatchPlan(3, T, 3).build(i32([300, 250, 150]), i32([2, 0, 1]))
+    pools = [D.DampPool("fp32", 3, H, d) for _ in range(3)]
+    for p in pools:
+        p.slots().fill_(0)
+    args = (plan, x["q"], x["k"], x["v"], x["alpha"], x["beta"] if rule == "delta" else None)
+    want = pools[0].prefill(*args, rule=rule)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(want) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, s, o in zip(pools[1:], streams, outs):
+            p.prefill(*args, o, rule=rule, stream=s)
+    torch.cuda.synchronize()
+    for p, o in zip(pools[1:], outs):
+        assert torch.equal(o, want) and torch.equal(p.slots(), pools[0].slots())
+
+
+def test_refusals_with_a_device_pool():
+    H, d, T = 2, 128, 8
+    x = inputs(torch.Generator().manual_seed(1), T, H, H, d, d, BF)
+    pool = D.DampPool("mixed", 3, H, d, np.array([[0, 5], [7, 9]]))
+    plan = D.BatchPlan(1, T, 3).build(i32([T]), i32([0]))
+    ok = dict(plan=plan, q=x["q"], k=x["k"], v=x["v"], alpha=x["alpha"], beta=x["beta"])
+    for bad in (dict(q=x["q"].float()), dict(k=x["k"].float()), dict(beta=None), dict(rule="decay"),
+                dict(alpha=x["alpha"].half()), dict(alpha=x["alpha"][:, :1]),
+                dict(q=x["q"][..., ::2]), dict(plan=D.BatchPlan(1, T, 4)), dict(plan=D.BatchPlan(1, T + 1, 3)),
+                dict(out=torch.zeros(T, H, d, device="cuda")), dict(rule="gated")):
+        with pytest.raises((ValueError, KeyError)):
+            pool.prefill(**{**ok, **bad})
+    need = D.damp_prefill_workspace(pool.handle, D.DAMP_RULE_DELTA, 1, T, D.DAMP_DTYPE_BF16)
+    with pytest.raises(D.DampError) as e:
+        pool.prefill(**ok, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == D.DAMP_ERR_BUFFER_TOO_SMALL
+    with pytest.raises(D.DampError) as e:
+        pool.prefill(**ok, workspace=torch.empty(need + 256, dtype=torch.uint8, device="cuda")[16:])
+    assert e.value.status == D.DAMP_ERR_MISALIGNED
+    odd = torch.zeros(T, H * d + 4, dtype=BF, device="cuda")[:, :H * d].view(T, H, d)
+    with pytest.raises(D.DampError) as e:                          # rows not 16 bytes apart
+        pool.prefill(**{**ok, "v": odd})
+    assert e.value.status == D.DAMP_ERR_MISALIGNED
+    with pytest.raises(D.DampError) as e:                          # every row the same one
+        pool.prefill(**{**ok, "v": x["v"][:1].expand(T, H, d)})
+    assert e.value.status == D.DAMP_ERR_INVALID_ARGUMENT
+    pool.prefill(**ok, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert pool.get_error() == 0
+    pool.close()
