@@ -273,6 +273,8 @@ int damp_decay_step(const damp_pool* pool, int n, const int32_t* slot_idx, int i
  *                       behind the last request)
  *   token_pos  [max_tokens]  past + position in its request (-1 behind the
  *                       last).  Both token maps may be NULL; 16-byte aligned.
+ *   order [n]           the requests, longest first (ties: lower first; above
+ *                       1024 requests: as they come).  May be NULL.
  *   totals [4]          {rows, blocks, longest request, DAMP_PLAN_EFLAG_* bits}
  * A negative length or past counts as 0 (DAMP_PLAN_EFLAG_VALUE).  A request
  * whose rows would end behind max_tokens is dropped together with every later
@@ -290,13 +292,15 @@ int damp_plan_blocks(int n, int max_tokens, int* max_blocks);
 int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const int32_t* slot_idx,
                     int n_slots, int max_tokens, int32_t* cu_seqlens, int32_t* load_slot,
                     int32_t* store_slot, int32_t* block_table, int32_t* token_slot,
-                    int32_t* token_pos, int32_t* totals, void* stream);
+                    int32_t* token_pos, int32_t* order, int32_t* totals, void* stream);
 
 /*
  * The prompts of a planned batch through one layer: every token's readout, and
  * every request's state left in its pool slot, ready for damp_decode_step
  * (DAMP_RULE_DELTA) or damp_decay_step (DAMP_RULE_DECAY).
- *   n, max_tokens, cu_seqlens, load_slot, store_slot, block_table : the plan
+ *   n, max_tokens, cu_seqlens, load_slot, store_slot, block_table, order : the
+ *           plan (order: a permutation of the requests, the order in which their
+ *           work is started; NULL: as they come)
  *   q, k  : device [max_tokens][H_qk][d_k], v: device [max_tokens][H][d_v],
  *           bf16 or float32 (in_dtype), heads and channels dense; *_stride =
  *           elements between token rows (views of one projection's output are
@@ -327,8 +331,8 @@ int damp_prefill_workspace(const damp_pool* pool, int rule, int n, int max_token
                            size_t* bytes);
 int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
                  const int32_t* cu_seqlens, const int32_t* load_slot, const int32_t* store_slot,
-                 const int32_t* block_table, int in_dtype, int H_qk, const void* q,
-                 int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 const int32_t* block_table, const int32_t* order, int in_dtype, int H_qk,
+                 const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                  int64_t v_stride, const float* alpha, const float* beta, void* out,
                  void* workspace, size_t workspace_bytes, void* stream);
 

@@ -96,9 +96,9 @@ def _load():
         "damp_calib_select_budget_static": (I, [I, I, I, P, P, P, P]),
         "damp_decay_step": (I, [P, I, P, I, I, P, P, P, P, P, P]),
         "damp_plan_blocks": (I, [I, I, ctypes.POINTER(I)]),
-        "damp_batch_plan": (I, [I, P, P, P, I, I, P, P, P, P, P, P, P, P]),
+        "damp_batch_plan": (I, [I, P, P, P, I, I, P, P, P, P, P, P, P, P, P]),
         "damp_prefill_workspace": (I, [P, I, I, I, I, ctypes.POINTER(S)]),
-        "damp_prefill": (I, [P, I, I, I, P, P, P, P, I, I, P, L, P, L, P, L, P, P, P, P, S, P]),
+        "damp_prefill": (I, [P, I, I, I, P, P, P, P, P, I, I, P, L, P, L, P, L, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -491,13 +491,13 @@ def damp_plan_blocks(n: int, max_tokens: int) -> int:
 def damp_batch_plan(lengths: torch.Tensor, slot_idx: torch.Tensor, past, n_slots: int,
                     max_tokens: int, cu_seqlens: torch.Tensor, load_slot: torch.Tensor,
                     store_slot: torch.Tensor, block_table: torch.Tensor, token_slot, token_pos,
-                    totals: torch.Tensor, stream=None) -> None:
+                    order, totals: torch.Tensor, stream=None) -> None:
     """Index arrays of a ragged batch from its lengths (all int32, on one
     device).  lengths, slot_idx [n]; past [n] or None; outputs cu_seqlens
     [n+1], load_slot [n], store_slot [n], block_table
     [damp_plan_blocks(n, max_tokens)][4], token_slot and token_pos
-    [max_tokens] (or both None), totals [4] = rows, blocks, longest request,
-    DAMP_PLAN_EFLAG_* bits."""
+    [max_tokens] (or both None), order [n] (or None) = the requests, longest
+    first, totals [4] = rows, blocks, longest request, DAMP_PLAN_EFLAG_* bits."""
     if not isinstance(lengths, torch.Tensor) or lengths.dim() != 1:
         raise ValueError("lengths must be a 1-D tensor")
     n = lengths.numel()
@@ -513,6 +513,7 @@ def damp_batch_plan(lengths: torch.Tensor, slot_idx: torch.Tensor, past, n_slots
             _want(block_table, "block_table", (damp_plan_blocks(n, max_tokens), 4), i32, dev),
             None if token_slot is None else _want(token_slot, "token_slot", (max_tokens,), i32, dev),
             None if token_pos is None else _want(token_pos, "token_pos", (max_tokens,), i32, dev),
+            None if order is None else _want(order, "order", (n,), i32, dev),
             _want(totals, "totals", (4,), i32, dev))
     with _on_device(dev):
         _check(_lib.damp_batch_plan(n, *ptr, n_slots, max_tokens, *outs, _launch_stream(stream, dev)),
@@ -536,7 +537,7 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
 
 
 def damp_prefill(pool: int, rule: int, cu_seqlens: torch.Tensor, load_slot: torch.Tensor,
-                 store_slot: torch.Tensor, block_table: torch.Tensor, q: torch.Tensor,
+                 store_slot: torch.Tensor, block_table: torch.Tensor, order, q: torch.Tensor,
                  k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor, beta, out: torch.Tensor,
                  workspace=None, stream=None) -> None:
     """The prompts of a planned batch through one layer (DAMP_RULE_DELTA or
@@ -564,7 +565,8 @@ def damp_prefill(pool: int, rule: int, cu_seqlens: torch.Tensor, load_slot: torc
     ints = (_want(cu_seqlens, "cu_seqlens", (n + 1,), i32, dev),
             _want(load_slot, "load_slot", (n,), i32, dev),
             _want(store_slot, "store_slot", (n,), i32, dev),
-            _want(block_table, "block_table", (damp_plan_blocks(n, T), 4), i32, dev))
+            _want(block_table, "block_table", (damp_plan_blocks(n, T), 4), i32, dev),
+            None if order is None else _want(order, "order", (n,), i32, dev))
     ends = (_want(alpha, "alpha", (T, H), f32, dev),
             None if beta is None else _want(beta, "beta", (T, H), f32, dev),
             _want(out, "out", (T, H, d_v), kind, dev))
@@ -713,13 +715,13 @@ class BatchPlan:
         self.max_blocks = damp_plan_blocks(n, max_tokens)
         e = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)  # noqa: E731
         self.cu_seqlens, self.load_slot, self.store_slot = e(n + 1), e(n), e(n)
-        self.block_table, self.totals = e(self.max_blocks, 4), e(4)
+        self.block_table, self.order, self.totals = e(self.max_blocks, 4), e(n), e(4)
         self.token_slot, self.token_pos = (e(max_tokens), e(max_tokens)) if token_maps \
             else (None, None)
         # the buffers stay this object's own: their addresses are looked up once
         self._out = [None if t is None else t.data_ptr()
                      for t in (self.cu_seqlens, self.load_slot, self.store_slot, self.block_table,
-                               self.token_slot, self.token_pos, self.totals)]
+                               self.token_slot, self.token_pos, self.order, self.totals)]
 
     def build(self, lengths: torch.Tensor, slot_idx: torch.Tensor, past=None, stream=None):
         """Index arrays of requests with ``lengths`` tokens each, ``past``
@@ -831,7 +833,8 @@ class DampPool:
             with _alloc_stream(stream, v.device):
                 out = torch.zeros_like(v, memory_format=torch.contiguous_format)
         damp_prefill(self.handle, RULES[rule] if isinstance(rule, str) else rule, plan.cu_seqlens,
-                     plan.load_slot, plan.store_slot, plan.block_table, q, k, v, alpha, beta, out,
+                     plan.load_slot, plan.store_slot, plan.block_table, plan.order, q, k, v, alpha,
+                     beta, out,
                      workspace, stream)
         return out
 

@@ -498,7 +498,7 @@ int damp_plan_blocks(int n, int max_tokens, int* max_blocks) {
 int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const int32_t* slot_idx,
                     int n_slots, int max_tokens, int32_t* cu_seqlens, int32_t* load_slot,
                     int32_t* store_slot, int32_t* block_table, int32_t* token_slot,
-                    int32_t* token_pos, int32_t* totals, void* stream) {
+                    int32_t* token_pos, int32_t* order, int32_t* totals, void* stream) {
     damp::PlanArgs a{};
     const int rc = damp_plan_blocks(n, max_tokens, &a.max_blocks);
     if (rc) return rc;
@@ -509,7 +509,7 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
     if (a.max_blocks > 0 && !block_table) return DAMP_ERR_INVALID_ARGUMENT;
     if (!aligned16(block_table) || !aligned16(token_slot) || !aligned16(token_pos))
         return DAMP_ERR_MISALIGNED;
-    const void* words[] = {lengths, past, slot_idx, cu_seqlens, load_slot, store_slot, totals};
+    const void* words[] = {lengths, past, slot_idx, cu_seqlens, load_slot, store_slot, order, totals};
     for (const void* w : words)
         if (reinterpret_cast<uintptr_t>(w) & 3u) return DAMP_ERR_MISALIGNED;
     a.lengths = lengths;
@@ -524,6 +524,7 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
     a.block_table = block_table;
     a.token_slot = token_slot;
     a.token_pos = token_pos;
+    a.order = order;
     a.totals = totals;
     return cuda_status(damp::launch_plan(a, static_cast<cudaStream_t>(stream)));
 }
@@ -576,7 +577,8 @@ int damp_prefill_workspace(const damp_pool* pool, int rule, int n, int max_token
 
 int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
                  const int32_t* cu_seqlens, const int32_t* load_slot, const int32_t* store_slot,
-                 const int32_t* block_table, int in_dtype, int H_qk, const void* q,
+                 const int32_t* block_table, const int32_t* order, int in_dtype, int H_qk,
+                 const void* q,
                  int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                  int64_t v_stride, const float* alpha, const float* beta, void* out,
                  void* workspace, size_t workspace_bytes, void* stream) {
@@ -598,7 +600,7 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
         !aligned16(block_table) || (q_stride * esz) % 16 || (k_stride * esz) % 16 ||
         (v_stride * esz) % 16)
         return DAMP_ERR_MISALIGNED;
-    const void* words[] = {cu_seqlens, load_slot, store_slot, alpha, beta};
+    const void* words[] = {cu_seqlens, load_slot, store_slot, order, alpha, beta};
     for (const void* p : words)
         if (reinterpret_cast<uintptr_t>(p) & 3u) return DAMP_ERR_MISALIGNED;
     if (w.total) {
@@ -611,6 +613,7 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
     a.load_slot = load_slot;
     a.store_slot = store_slot;
     a.block_table = block_table;
+    a.order = order;
     a.q = q;
     a.k = k;
     a.v = v;

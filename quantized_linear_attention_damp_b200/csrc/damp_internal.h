@@ -133,6 +133,7 @@ struct PlanArgs {
     int32_t* token_slot;       // [max_tokens] (both token maps or neither)
     int32_t* token_pos;        // [max_tokens]
     int32_t* totals;           // [4]
+    int32_t* order;            // [n] or NULL
 };
 
 // Arguments of the prefill kernels (damp_prefill.cu, damp_prefill_chunk.cu).
@@ -144,6 +145,7 @@ struct PrefillArgs {
     const int32_t* load_slot;
     const int32_t* store_slot;
     const int32_t* block_table;
+    const int32_t* order;      // [n] requests in the order in which they are started; NULL: as they come
     const void* q;
     const void* k;
     const void* v;

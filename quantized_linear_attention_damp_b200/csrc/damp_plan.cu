@@ -27,6 +27,7 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kRowsPerCta = 4 * kPlanThreads;   // token rows one CTA is given at least
 constexpr int kB = DAMP_PLAN_BLOCK;
+constexpr int kSorted = 1024;                   // requests up to which the order is by length
 
 // Smallest r with end[r] > x; `end` ascends and end[n - 1] > x.
 __device__ __forceinline__ int owner(const int* end, int n, int x) {
@@ -141,6 +142,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         a.totals[1] = btop;
         a.totals[2] = longest;
         a.totals[3] = bad;
+    }
+    // ---- order: longest first, so that a long prompt is not what a launch ends with.  n compares for
+    // each request; more requests than kSorted balance themselves and are taken as they come.
+    if (a.order) {
+        __shared__ __align__(16) int s_len[kSorted];
+        if (n <= kSorted) {
+            for (int r = tid; r < kSorted; r += kPlanThreads)
+                s_len[r] = r < n ? s_end[r] - (r ? s_end[r - 1] : 0) : -1;
+            __syncthreads();
+        }
+        for (int r = gtid; r < n; r += gsize) {
+            int rank = r;
+            if (n <= kSorted) {
+                const int mine = s_len[r];
+                rank = 0;
+                for (int j = 0; j < n; j += 4) {
+                    const int4 l = *reinterpret_cast<const int4*>(s_len + j);
+                    rank += (l.x > mine || (l.x == mine && j < r)) + (l.y > mine || (l.y == mine && j + 1 < r)) +
+                            (l.z > mine || (l.z == mine && j + 2 < r)) + (l.w > mine || (l.w == mine && j + 3 < r));
+                }
+            }
+            a.order[rank] = r;
+        }
     }
     // ---- per block
     for (int i = gtid; i < a.max_blocks; i += gsize) {

@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kTokThreads) prefill_tokens_kernel(const Prefi
     constexpr int CPC = kTokThreads / NL;       // columns a CTA owns
     extern __shared__ __align__(16) uint8_t sm[];
     const int tid = threadIdx.x, p = tid % NL, col = tid / NL;
-    const int r = blockIdx.x, h = blockIdx.y;
+    const int r = a.order ? __ldg(a.order + blockIdx.x) : blockIdx.x, h = blockIdx.y;
+    if (r < 0 || r >= a.n) return;
     const int j = blockIdx.z * CPC + col;       // this thread's value column
     const bool bf16 = a.bf16;
     const int end = min(max(__ldg(a.cu_seqlens + r + 1), 0), a.max_tokens);

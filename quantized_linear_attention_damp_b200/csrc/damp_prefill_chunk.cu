@@ -216,8 +216,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             }
             tc_commit(bar_mma);
         }
+        // one warp polls, the others wait at the barrier: polling takes shared-memory bandwidth
+        ok = ok && __all_sync(0xffffffffu, bounded_wait(bar_mma, 0, a.wait_ns, &s_abort, false));
     }
-    ok = ok && bounded_wait(bar_mma, 0, a.wait_ns, &s_abort, false);
     const bool fine = __syncthreads_and(ok);       // (a wait that ran out: nothing more is done)
     tc_fence_after();
     float* s_a = reinterpret_cast<float*>(sm + DPrep::a);
@@ -494,7 +495,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int req = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int at = blockIdx.x / a.H, h = blockIdx.x % a.H, req = a.order ? __ldg(a.order + at) : at;
+    if (req < 0 || req >= a.n) return;
     const int cu0 = __ldg(a.cu_seqlens + req), cu1 = __ldg(a.cu_seqlens + req + 1);
     const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req), block0 = ca.first_block[req];
     const int end = min(max(cu1, 0), a.max_tokens), start = min(max(cu0, 0), end), len = end - start;
@@ -868,8 +870,10 @@ __global__ void __launch_bounds__(EChain::threads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seg = blockIdx.x % sa.segs, unit = blockIdx.x / sa.segs;
-    const int req = unit / a.H, h = unit % a.H;
+    const int seg = blockIdx.x % sa.segs, place = blockIdx.x / sa.segs, h = place % a.H;
+    const int req = a.order ? __ldg(a.order + place / a.H) : place / a.H;
+    if (req < 0 || req >= a.n) return;
+    const int unit = req * a.H + h;
     const int cu0 = __ldg(a.cu_seqlens + req), cu1 = __ldg(a.cu_seqlens + req + 1);
     const int slot = __ldg(a.store_slot + req), from = __ldg(a.load_slot + req);
     const int end = min(max(cu1, 0), a.max_tokens), first = min(max(cu0, 0), end);

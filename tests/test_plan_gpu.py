@@ -41,14 +41,16 @@ def plain(lengths, past, slot, n_slots, T):
     full = np.full((D.damp_plan_blocks(n, T), 4), -1)
     if blocks:
         full[:blocks] = table
-    return dict(cu_seqlens=cu, load_slot=load, store_slot=store, block_table=full,
+    kept = np.diff(cu)
+    order = np.argsort(-kept, kind="stable") if n <= 1024 else np.arange(n)
+    return dict(cu_seqlens=cu, load_slot=load, store_slot=store, block_table=full, order=order,
                 token_slot=tslot, token_pos=tpos, totals=[cu[-1], blocks, longest, flags])
 
 
 def check(lengths, past, slot, n_slots, T, token_maps=True):
     i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
     p = D.BatchPlan(len(lengths), T, n_slots, token_maps=token_maps)
-    for t in (p.cu_seqlens, p.load_slot, p.store_slot, p.block_table, p.totals, p.token_slot,
+    for t in (p.cu_seqlens, p.load_slot, p.store_slot, p.block_table, p.order, p.totals, p.token_slot,
               p.token_pos):
         if t is not None:
             t.fill_(12345)

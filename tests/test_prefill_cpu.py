@@ -42,7 +42,7 @@ def test_plan_block_counts():
 
 def plan_args(**kw):
     a = dict(n=2, lengths=P16, past=None, slot_idx=P16, n_slots=4, max_tokens=100, cu=P16, load=P16,
-             store=P16, table=P16, tslot=P16, tpos=P16, totals=P16, stream=None)
+             store=P16, table=P16, tslot=P16, tpos=P16, order=None, totals=P16, stream=None)
     a.update(kw)
     return list(a.values())
 
@@ -52,7 +52,7 @@ def plan_args(**kw):
     (dict(slot_idx=None), INV), (dict(cu=None), INV), (dict(load=None), INV), (dict(store=None), INV),
     (dict(table=None), INV), (dict(totals=None), INV), (dict(tslot=None), INV), (dict(tpos=None), INV),
     (dict(table=ODD), MIS), (dict(tslot=ODD), MIS), (dict(tpos=ODD), MIS),
-    (dict(lengths=ctypes.c_void_p(4098)), MIS), (dict(n=D.DAMP_PLAN_MAX_REQUESTS + 1), UNS)])
+    (dict(lengths=ctypes.c_void_p(4098)), MIS), (dict(order=ctypes.c_void_p(4097)), MIS), (dict(n=D.DAMP_PLAN_MAX_REQUESTS + 1), UNS)])
 def test_plan_refuses(kw, rc):
     assert lib.damp_batch_plan(*plan_args(**kw)) == rc
 
@@ -69,7 +69,7 @@ def test_decay_step_refuses(host_pool):
 
 
 def prefill_args(pool, **kw):
-    a = dict(pool=pool, rule=0, n=2, T=10, cu=P16, load=P16, store=P16, table=P16, dt=0, hqk=3, q=P16,
+    a = dict(pool=pool, rule=0, n=2, T=10, cu=P16, load=P16, store=P16, table=P16, order=None, dt=0, hqk=3, q=P16,
              qs=384, k=P16, ks=384, v=P16, vs=768, alpha=P16, beta=P16, out=P16, ws=P16, wsb=1 << 40,
              stream=None)
     a.update(kw)
@@ -107,16 +107,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(host_pool):
         with pytest.raises(ValueError):
             D.damp_decay_step(host_pool, **{**good, **bad})
     pre = dict(rule=0, cu_seqlens=i(3), load_slot=i(2), store_slot=i(2),
-               block_table=i((D.damp_plan_blocks(2, 5), 4)), q=q, k=q, v=v, alpha=z(5, 6),
+               block_table=i((D.damp_plan_blocks(2, 5), 4)), order=None, q=q, k=q, v=v, alpha=z(5, 6),
                beta=z(5, 6), out=z(5, 6, 128))
     for bad in (dict(), dict(rule=7), dict(q=z(5, 4, 128)), dict(v=z(5, 5, 128)),
                 dict(beta=None), dict(rule=1), dict(alpha=z(5, 3)), dict(cu_seqlens=i(2))):
         with pytest.raises(ValueError):
             D.damp_prefill(host_pool, **{**pre, **bad})
     with pytest.raises(ValueError):
-        D.damp_batch_plan(i(2), i(2), None, 4, 10, i(3), i(2), i(2), i((2, 4)), None, None, i(4))
+        D.damp_batch_plan(i(2), i(2), None, 4, 10, i(3), i(2), i(2), i((2, 4)), None, None, None, i(4))
     with pytest.raises(ValueError):
-        D.damp_batch_plan(i((2, 1)), i(2), None, 4, 10, i(3), i(2), i(2), i((2, 4)), None, None, i(4))
+        D.damp_batch_plan(i((2, 1)), i(2), None, 4, 10, i(3), i(2), i(2), i((2, 4)), None, None, None, i(4))
 
 
 def test_token_rows_must_be_dense_inside():
