@@ -216,7 +216,8 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     const size_t smem = (size_t)a.n * 8;
-    if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    // (beside 5 KB of static shared memory)
+    if (smem > 40 * 1024 && (e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                       DAMP_PLAN_MAX_REQUESTS * 8)) != cudaSuccess)
         return e;
     const long long rows = std::max((long long)a.max_tokens, (long long)a.max_blocks);

@@ -1,4 +1,8 @@
 """damp_batch_plan against a loop over the requests."""
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -117,3 +121,17 @@ def test_captured_build_reads_new_lengths():
     want = plain(new, [0] * n, [0, 1, 2, 3, 4, 5], 8, T)
     for name, w in want.items():
         assert np.array_equal(getattr(p, name).cpu().numpy(), np.asarray(w)), name
+
+
+def test_first_build_of_a_process_with_many_requests():
+    """Offsets of 5,600 to 6,144 requests, with the kernel's own shared memory, just pass the 48 KB that a
+    launch has without asking for more; a larger build before would have asked already."""
+    code = """
+import torch, quantized_linear_attention_damp_b200 as D
+one = torch.ones(6144, dtype=torch.int32, device="cuda")
+for n in (5000, 5600, 6000, 6144):
+    p = D.BatchPlan(n, n, 1).build(one[:n], torch.zeros_like(one[:n]))
+    assert p.totals.tolist() == [n, n, 1, 0], (n, p.totals)
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300,
+                   cwd=Path(__file__).resolve().parent.parent)
