@@ -399,8 +399,11 @@ cudaError_t launch_square(const StepArgs& a, int H_qk, int bf16, cudaStream_t s)
 template <int KIND, int G, bool SOLO, bool ALL>
 cudaError_t launch_rows_f(const StepArgs& a, int ctas, int H_qk, int bf16, cudaStream_t s) {
     const auto f = decay_step_rows_kernel<KIND, G, SOLO, ALL>;
-    const int smem = Ring<G>::bytes + (SOLO ? kDecayThreads / 32 : 1) * a.d_k * 16;
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int base = Ring<G>::bytes, per_row = (SOLO ? kDecayThreads / 32 : 1) * 16;
+    const int smem = base + per_row * a.d_k;
+    // (the kernel's most, not this call's: another thread may be launching it too)
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               base + per_row * kMaxDim);
     if (e != cudaSuccess) return e;
     f<<<ctas, kDecayThreads, smem, s>>>(a, H_qk, bf16);
     return cudaGetLastError();

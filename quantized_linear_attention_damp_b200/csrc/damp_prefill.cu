@@ -223,7 +223,9 @@ cudaError_t launch_nl(const PrefillArgs& a, cudaStream_t s) {
     const dim3 grid(a.n, a.H, (a.d_v + CPC - 1) / CPC);
     const auto f = a.delta ? prefill_tokens_kernel<NL, R, true> : prefill_tokens_kernel<NL, R, false>;
     const int smem = TokSmem(NL, R, a.d_k, a.bf16 ? 2 : 4).bytes;
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the kernel's most, not this call's: another thread may be launching it too)
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               TokSmem(NL, R, NL * R, 4).bytes);
     if (e != cudaSuccess) return e;
     f<<<grid, kTokThreads, smem, s>>>(a);
     return cudaGetLastError();

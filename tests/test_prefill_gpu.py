@@ -1,4 +1,6 @@
 """damp_prefill against the token recurrence in 64 bits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -370,6 +372,39 @@ def test_two_calls_at_once(rule):
     torch.cuda.synchronize()
     for p, o in zip(pools[1:], outs):
         assert torch.equal(o, want) and torch.equal(p.slots(), pools[0].slots())
+
+
+@pytest.mark.parametrize("what", ["prefill", "step"])
+def test_two_host_threads(what):
+    """Two threads launch the same kernel with different amounts of shared memory."""
+    errors, start = [], threading.Barrier(2)
+
+    def run(d_k, dtype):
+        try:
+            g = torch.Generator().manual_seed(d_k)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                pool = D.DampPool("fp32", 2, 2, d_k, d_v=48)
+                pool.slots().fill_(0)
+                x = inputs(g, 2, 2, 2, d_k, 48, dtype)
+                plan = D.BatchPlan(2, 2, 2).build(i32([1, 1]), i32([1, 0]))
+                out = torch.empty(2, 2, 48, device="cuda")
+            start.wait()
+            for _ in range(400):
+                if what == "prefill":
+                    pool.prefill(plan, x["q"], x["k"], x["v"], x["alpha"], x["beta"], stream=stream)
+                else:
+                    pool.decay_step(plan.store_slot, x["q"], x["k"], x["v"], x["alpha"], out, stream=stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=a) for a in ((144, BF), (256, torch.float32))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
 
 
 def test_refusals_with_a_device_pool():
