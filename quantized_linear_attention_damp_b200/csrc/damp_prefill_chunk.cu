@@ -1132,22 +1132,26 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             if (!wait_group(warp == X::wOut, X::BO + (c & 1), (c >> 1) & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             // (Not unrolled, as other long loops of this kernel are not: two SMs share an instruction
-            // cache that the unrolled roles together do not fit.  16 ragged requests of 8192 tokens,
-            // 32 heads: 131 us unrolled, 125 so.  The delta chain, whose roles wait for one another,
+            // cache that the unrolled roles together do not fit: 16 ragged requests of 8192 tokens,
+            // 32 heads, took 131 us unrolled and 125 so.  The delta chain, whose roles wait for one another,
             // is slower so: 430 us against 460 for 4096 tokens.)
 #pragma unroll 1
             for (int part = 0; part < 4; ++part) {
                 uint32_t o1[16], o2[16];
                 tmem_ld16(lanes + X::O1 + part * 16, o1);
                 tmem_ld16(lanes + X::O2 + part * 16, o2);
+                float2 gt[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gt[i] = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
                 tmem_wait_ld();
+                // (the loader may write over these decays once the block after next is loaded, which
+                // this arrival lets happen: they are read before it)
                 if (part == 3) arrive(X::CO);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 gt = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
                     const uint32_t o = pack_bf16(
-                        __fmaf_rn(gt.x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
-                        __fmaf_rn(gt.y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
+                        __fmaf_rn(gt[i].x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
+                        __fmaf_rn(gt[i].y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
                     uint8_t* to = so + (part * 16 + 2 * i) * X::out_row + vcol * 2;
                     *reinterpret_cast<uint16_t*>(to) = (uint16_t)o;
                     *reinterpret_cast<uint16_t*>(to + X::out_row) = (uint16_t)(o >> 16);
