@@ -639,28 +639,40 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                 v[i] = __uint_as_float((uint32_t)b << 16);
             }
             uint32_t x[16], h8[8], l8[8];
+            // (the decays of R behind the wait, the factors of U ahead of theirs, as measured: with both
+            // ahead a thread's registers do not suffice, 450 us against 418 for 8192 tokens x 32 heads)
             if (!(ok = wait_group(warp == 0, X::BK, ph, 4, X::kWarps * 32))) break;
             tc_fence_after();
             tmem_ld16(lanes + X::KQ + part * 16, x);
+            float g[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = reinterpret_cast<const float4*>(gam + part * 16)[i];
+                g[4 * i] = f.x, g[4 * i + 1] = f.y, g[4 * i + 2] = f.z, g[4 * i + 3] = f.w;
+            }
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                split_bf16(__fmaf_rn(-gam[part * 16 + 2 * i], __uint_as_float(x[2 * i]), v[2 * i]),
-                           __fmaf_rn(-gam[part * 16 + 2 * i + 1], __uint_as_float(x[2 * i + 1]), v[2 * i + 1]),
-                           h8[i], l8[i]);
+                split_bf16(__fmaf_rn(-g[2 * i], __uint_as_float(x[2 * i]), v[2 * i]),
+                           __fmaf_rn(-g[2 * i + 1], __uint_as_float(x[2 * i + 1]), v[2 * i + 1]), h8[i], l8[i]);
             tmem_st8(lanes + X::Rh + part * 8, h8);
             tmem_st8(lanes + X::Rh + 32 + part * 8, l8);
             tmem_wait_st();
             arrive(X::CR);
             // ---- diag(w) U as a pair
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = reinterpret_cast<const float4*>(w + part * 16)[i];
+                g[4 * i] = f.x, g[4 * i + 1] = f.y, g[4 * i + 2] = f.z, g[4 * i + 3] = f.w;
+            }
             if (!(ok = wait_group(warp == 0, X::BU, ph, 4, X::kWarps * 32))) break;
             tc_fence_after();
             tmem_ld16(lanes + X::UO + part * 16, x);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                split_bf16(w[part * 16 + 2 * i] * __uint_as_float(x[2 * i]),
-                           w[part * 16 + 2 * i + 1] * __uint_as_float(x[2 * i + 1]), h8[i], l8[i]);
+                split_bf16(g[2 * i] * __uint_as_float(x[2 * i]), g[2 * i + 1] * __uint_as_float(x[2 * i + 1]), h8[i],
+                           l8[i]);
             tmem_st8(lanes + X::Uh + part * 8, h8);
             tmem_st8(lanes + X::Ul + part * 8, l8);
             const float gc = gam[C - 1];
@@ -694,27 +706,28 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             if (!wait_group(warp == X::kWarps, X::BO, c & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             // out of TMEM first: the next block's Q S waits for that
-            uint32_t o[C / 2];
-#pragma unroll
+#pragma unroll 1
             for (int part = 0; part < 4; ++part) {
                 uint32_t o1[16], o2[16];
                 tmem_ld16(lanes + X::KQ + 64 + part * 16, o1);
                 tmem_ld16(lanes + X::UO + 64 + part * 16, o2);
+                float2 gt[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gt[i] = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
                 tmem_wait_ld();
+                if (part == 3) {
+                    arrive(X::CO);
+                    if (lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 gt = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
-                    o[part * 8 + i] = pack_bf16(
-                        __fmaf_rn(gt.x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
-                        __fmaf_rn(gt.y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
+                    const uint32_t o = pack_bf16(
+                        __fmaf_rn(gt[i].x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
+                        __fmaf_rn(gt[i].y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
+                    uint8_t* to = so + (part * 16 + 2 * i) * X::out_row + vcol * 2;
+                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)o;
+                    *reinterpret_cast<uint16_t*>(to + X::out_row) = (uint16_t)(o >> 16);
                 }
-            }
-            arrive(X::CO);
-            if (lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
-#pragma unroll
-            for (int i = 0; i < C / 2; ++i) {
-                *reinterpret_cast<uint16_t*>(so + 2 * i * X::out_row + vcol * 2) = (uint16_t)o[i];
-                *reinterpret_cast<uint16_t*>(so + (2 * i + 1) * X::out_row + vcol * 2) = (uint16_t)(o[i] >> 16);
             }
             bar_sync(1, X::kOut * 32);
             const int live = min(C, len - c * C);
@@ -1132,9 +1145,10 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             if (!wait_group(warp == X::wOut, X::BO + (c & 1), (c >> 1) & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             // (Not unrolled, as other long loops of this kernel are not: two SMs share an instruction
-            // cache that the unrolled roles together do not fit: 16 ragged requests of 8192 tokens,
-            // 32 heads, took 131 us unrolled and 125 so.  The delta chain, whose roles wait for one another,
-            // is slower so: 430 us against 460 for 4096 tokens.)
+            // cache that the unrolled roles together do not fit.  16 ragged requests of 8192 tokens,
+            // 32 heads: 131 us unrolled, 125 so.  The delta chain's roles wait for one another most of
+            // the time, and only its readout is better off: with its other loops not unrolled either,
+            // 8192 tokens x 32 heads took 460 us against 430.)
 #pragma unroll 1
             for (int part = 0; part < 4; ++part) {
                 uint32_t o1[16], o2[16];
