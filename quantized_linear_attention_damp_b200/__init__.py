@@ -718,6 +718,7 @@ class BatchPlan:
         self.block_table, self.order, self.totals = e(self.max_blocks, 4), e(n), e(4)
         self.token_slot, self.token_pos = (e(max_tokens), e(max_tokens)) if token_maps \
             else (None, None)
+        self.built = False
         # the buffers stay this object's own: their addresses are looked up once
         self._out = [None if t is None else t.data_ptr()
                      for t in (self.cu_seqlens, self.load_slot, self.store_slot, self.block_table,
@@ -733,6 +734,7 @@ class BatchPlan:
         with _on_device(dev):
             _check(_lib.damp_batch_plan(n, *ptr, self.n_slots, self.max_tokens, *self._out,
                                         _launch_stream(stream, dev)), "damp_batch_plan")
+        self.built = True
         return self
 
 
@@ -826,6 +828,10 @@ class DampPool:
         returns ``out`` (allocated, zero-filled, when None)."""
         if isinstance(q, torch.Tensor) and q.dim() == 3 and q.shape[0] != plan.max_tokens:
             raise ValueError(f"the plan is for {plan.max_tokens} token rows, got {q.shape[0]}")
+        if not plan.built:
+            raise ValueError("the plan has not been built")
+        if isinstance(rule, str) and rule not in RULES:
+            raise ValueError(f"unknown rule {rule!r}")
         if plan.n_slots > self.n_slots:
             raise ValueError(f"the plan allows slots up to {plan.n_slots}, the pool has "
                              f"{self.n_slots}")
@@ -834,8 +840,7 @@ class DampPool:
                 out = torch.zeros_like(v, memory_format=torch.contiguous_format)
         damp_prefill(self.handle, RULES[rule] if isinstance(rule, str) else rule, plan.cu_seqlens,
                      plan.load_slot, plan.store_slot, plan.block_table, plan.order, q, k, v, alpha,
-                     beta, out,
-                     workspace, stream)
+                     beta, out, workspace, stream)
         return out
 
     def get_error(self, clear=False, stream=None) -> int:

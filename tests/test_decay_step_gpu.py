@@ -119,3 +119,29 @@ def test_captured_steps_on_another_stream():
     side.synchronize()
     assert torch.equal(outs[0], outs[1])
     assert torch.equal(pools[0].slots(), pools[1].slots())
+
+
+@pytest.mark.parametrize("fmt", ["fp32", "mixed", "fp8"])
+def test_slots_past_32_bits(fmt):
+    """Slots behind 4 GiB of others give bit for bit what a small pool gives (5120 states, a warp each,
+    and 256, a CTA each)."""
+    H, d = 128, 128
+    g = torch.Generator().manual_seed(3)
+    rows = np.stack([np.arange(h % 4, 108, 4) for h in range(H)]) if fmt == "mixed" else None
+    for n in (40, 2):
+        small = D.DampPool(fmt, n, H, d, rows)
+        n_slots = (1 << 32) // (small.nbytes // n) + n + 2
+        big = D.DampPool(fmt, n_slots, H, d, rows)
+        S0 = torch.randn(n, H, d, d, generator=g).cuda()
+        at = [torch.arange(a, a + n, dtype=torch.int32, device="cuda") for a in (0, n_slots - n)]
+        x = [torch.randn(n, H, d, generator=g).bfloat16().cuda() for _ in range(3)]
+        alpha = torch.rand(n, H, generator=g).cuda()
+        out = [torch.empty(n, H, d, device="cuda") for _ in range(2)]
+        for pool, slots, o in zip((small, big), at, out):
+            pool.slots()[slots[0]:slots[-1] + 1] = 0      # (bytes between blocks are no one's)
+            pool.pack(slots, S0)
+            pool.decay_step(slots, *x, alpha, o)
+            assert pool.get_error() == 0
+        assert torch.equal(*out)
+        assert torch.equal(small.slots(), big.slots()[n_slots - n:])
+        small.close(), big.close()

@@ -353,6 +353,40 @@ def test_segments_of_long_requests():
 
 
 @pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_offsets_past_32_bits(rule, dtype, d):
+    """A request behind 4 GiB of token rows, its state behind 4 GiB of slots."""
+    H, first, L = 128, 1 << 17, 70
+    n_slots = (1 << 32) // (H * d * d * 4) + 2
+    g = torch.Generator().manual_seed(d)
+    x = inputs(g, L, H, 2, d, d, dtype)
+
+    def behind(t):
+        big = torch.zeros(first + L, *t.shape[1:], dtype=t.dtype, device="cuda")
+        big[first:] = t
+        return big
+
+    pool = D.DampPool("fp32", n_slots, H, d)
+    S0 = 0.3 * torch.randn(H, d, d, generator=g).cuda()
+    pool.pack(i32([n_slots - 1]), S0[None])
+    plan = D.BatchPlan(2, first + L, n_slots).build(i32([first, L]), i32([-1, n_slots - 1]), i32([0, 1]))
+    out = torch.ones(first + L, H, d, dtype=dtype, device="cuda")
+    pool.prefill(plan, behind(x["q"]), behind(x["k"]), behind(x["v"]), behind(x["alpha"]),
+                 behind(x["beta"]) if rule == "delta" else None, out, rule=rule)
+    assert not out[:64].any() and not out[first - 64:first].any()
+    o, S, top = recurrence(rule, x["q"], x["k"], x["v"], x["alpha"], x["beta"], S0)
+    S1 = torch.empty(1, H, d, d, device="cuda")
+    pool.unpack(i32([n_slots - 1]), S1)
+    tol = tolerance(L, d, dtype == BF) * top
+    assert ((S1[0].double() - S).flatten(1).norm(dim=1) <= tol).all()
+    qn = x["q"].double().norm(dim=-1).repeat_interleave(H // 2, dim=1)
+    lim = (EPS_BF16 if dtype == BF else EPS32) * o.abs() + ((tol + d * EPS32 * top)[None] * qn)[..., None]
+    assert ((out[first:].double() - o).abs() <= lim).all()
+    assert pool.get_error() == 0
+    pool.close()
+
+
+@pytest.mark.parametrize("rule", RULES)
 def test_two_calls_at_once(rule):
     """Two layers on two streams at the same time, each with its own pool and workspace."""
     H, d, T = 4, 128, 700
@@ -419,6 +453,8 @@ def test_refusals_with_a_device_pool():
                 dict(out=torch.zeros(T, H, d, device="cuda")), dict(rule="gated")):
         with pytest.raises((ValueError, KeyError)):
             pool.prefill(**{**ok, **bad})
+    with pytest.raises(ValueError, match="not been built"):
+        pool.prefill(**{**ok, "plan": D.BatchPlan(1, T, 3)})
     need = D.damp_prefill_workspace(pool.handle, D.DAMP_RULE_DELTA, 1, T, D.DAMP_DTYPE_BF16)
     with pytest.raises(D.DampError) as e:
         pool.prefill(**ok, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
