@@ -100,11 +100,14 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 // TMEM as the A operand of G = P T'.  The inverse is FP32 arithmetic of the
 // ordinary kind: an error of it is an error of the state.  Q and K share their
 // 32 KB with A and T (FP32) and then with the finished record.
-// (Products by mma.sync, staged by the threads: 97 us for 4096 units; this 83.)
+// (4096 units: 83 us; with products by mma.sync, staged by the threads, 97.
+// With P handed over in shared memory, so that 64 columns of TMEM are enough:
+// no faster with 5 CTAs an SM than with 4, slower with 6, whose 80 registers
+// do not suffice.)
 
 // The record of one (block, head): C x C bf16 matrices with 128-byte rows
-// (K-major, 128-byte swizzle) in the order in which the chain's products take
-// them as one operand of 128 rows, then gamma_t and gamma_C / gamma_t.
+// (K-major, 128-byte swizzle) as the chain's products take them, then gamma_t
+// and gamma_C / gamma_t.
 struct DRec {
     static constexpr int th = 0, gh = kMat, tl = 2 * kMat, gl = 3 * kMat;   // T' hi, G hi, T' lo, G lo
     static constexpr int gam = 4 * kMat, w = gam + 4 * C;
@@ -1329,7 +1332,8 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int heads, long long rows, 
 // Segments of a request for the decay rule: as many as the SMs have room for,
 // none shorter (on average) than 4 blocks; a batch whose (request, head) pairs
 // take more than half of the SMs stays whole (the first pass reads K and V once
-// more).  One prompt of 4096 tokens x 32 heads: 81 us in 4 segments, 187 whole.
+// more).  One prompt of 4096 tokens x 32 heads: 74 us in 4 segments, 119 in 2,
+// 158 whole.
 int decay_segments(int n, int H, int max_tokens, int sms) {
     const long long chains = (long long)n * H;
     if (chains * 2 > sms) return 1;
