@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libdamp.so")
 SOURCES = ["damp_abi.cu", "damp_decode.cu", "damp_decode_unit.cu", "damp_decode_any.cu",
            "damp_codec.cu", "damp_calib.cu", "damp_plan.cu", "damp_decay_step.cu",
            "damp_prefill.cu", "damp_prefill_chunk.cu"]
-HEADERS = ["damp_internal.h", "damp_device.cuh", "damp_tcgen05.cuh"]
+HEADERS = ["damp_internal.h", "damp_prompt.h", "damp_device.cuh", "damp_tcgen05.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",

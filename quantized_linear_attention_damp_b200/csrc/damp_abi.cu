@@ -15,6 +15,7 @@
 
 #include "damp.h"
 #include "damp_internal.h"
+#include "damp_prompt.h"
 
 using damp::PoolDesc;
 

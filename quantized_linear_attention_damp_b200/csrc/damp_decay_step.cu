@@ -15,6 +15,7 @@
 
 #include "damp.h"
 #include "damp_device.cuh"
+#include "damp_prompt.h"
 
 namespace damp {
 namespace {

@@ -42,6 +42,20 @@ __device__ __forceinline__ float in_val(const void* base, size_t idx, bool bf16)
     return static_cast<const float*>(base)[idx];
 }
 
+// Value of one E4M3 code (exact).
+__device__ __forceinline__ float e4m3_value(uint8_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+}
+
+// E4M3 code of y (nearest, ties to even, saturating at 448).
+__device__ __forceinline__ uint8_t e4m3_code(float y) {
+    unsigned short p;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(0.0f), "f"(y));
+    return (uint8_t)(p & 0xffu);
+}
+
 // Element j of stored row i, before the decay: S^_ij.  codec: 0 FP32 state,
 // 1 INT8 rows, 2 FP8 rows; e = the row's directory word; s = its scale.
 __device__ __forceinline__ float load_shat(const uint8_t* blk, int codec, uint32_t e, float s,

@@ -241,20 +241,6 @@ __device__ __forceinline__ uint32_t quant_e4m3x4(float2 lo, float2 hi, float inv
     return inv == 0.0f ? 0u : ((uint32_t)p01 | ((uint32_t)p23 << 16));
 }
 
-// Value of one E4M3 code (exact).
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
-}
-
-// E4M3 code of y (nearest, ties to even, saturating at 448).
-__device__ __forceinline__ uint8_t e4m3_code(float y) {
-    unsigned short p;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(0.0f), "f"(y));
-    return (uint8_t)(p & 0xffu);
-}
-
 // Requantize rows [r0, r0+RPT) of x into a quantized block at `blk` (shared or
 // global).  rowbuf: 2*RPT floats private to this row group (shared memory).
 // Must be called by every lane of the warp (it synchronises the warp).

@@ -19,6 +19,7 @@
 
 #include "damp.h"
 #include "damp_internal.h"
+#include "damp_prompt.h"
 
 namespace damp {
 namespace {

@@ -22,6 +22,7 @@
 
 #include "damp.h"
 #include "damp_device.cuh"
+#include "damp_prompt.h"
 
 namespace damp {
 namespace {

@@ -37,6 +37,7 @@
 
 #include "damp.h"
 #include "damp_tcgen05.cuh"
+#include "damp_prompt.h"
 
 namespace damp {
 namespace {
