@@ -280,6 +280,7 @@ int damp_decay_step(const damp_pool* pool, int n, const int32_t* slot_idx, int i
  * whose rows would end behind max_tokens is dropped together with every later
  * request that has rows (DAMP_PLAN_EFLAG_TOKENS): no rows, slots -1.  A slot
  * >= n_slots counts as padding (DAMP_PLAN_EFLAG_SLOT).
+ * No output may overlap an input.
  * Limits: n <= DAMP_PLAN_MAX_REQUESTS, max_tokens <= DAMP_PLAN_MAX_TOKENS.
  */
 #define DAMP_PLAN_BLOCK 64
@@ -319,6 +320,8 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
  * States are FP32 inside the call: a quantized pool's are dequantized before it
  * and quantized once after it (damp_pool_unpack / damp_pool_pack).
  * Inputs are finite; a request's values reach no other request's results.
+ * out and workspace overlap no input.  Limits (DAMP_ERR_UNSUPPORTED): the
+ * plan's, H <= 65535, and n * H and blocks * H below 2^31.
  * Arithmetic: FP32, token by token, and the readout rounded once; bf16 layers
  * with d_k = d_v = 128 run in blocks of 64 tokens on the tensor cores, where
  * every FP32 operand enters as two bf16 values (2^-17 of it are lost): states
