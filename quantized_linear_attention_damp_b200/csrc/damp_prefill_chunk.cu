@@ -9,22 +9,23 @@
 //                O  = diag(gamma) Q S + (Q K^T o Gamma) U       (s <= t)
 //                S <- gamma_C S + K^T diag(gamma_C / gamma) U
 //   decay rule:  the same with U = V.
-// Two kernels:
+// delta: two kernels.
 //   prepare (one CTA per block and head, no order between blocks): everything
-//     that does not depend on S.  T' = (I + A)^-1 diag(beta), then
-//     G = (Q K^T o Gamma) T' and T~ = diag(gamma_C / gamma) T', so that with
-//     R = V - diag(gamma) K S:  O = diag(gamma) Q S + G R and
-//     S <- gamma_C S + K^T (T~ R).  The decay rule needs P = Q K^T o Gamma.
+//     that does not depend on S.  T' = (I + A)^-1 diag(beta) and
+//     G = (Q K^T o Gamma) T', so that with R = V - diag(gamma) K S and
+//     U = T' R:  O = diag(gamma) Q S + G R and
+//     S <- gamma_C S + K^T diag(gamma_C / gamma) U.
 //   chain (one CTA per request and head, blocks in order): the products with
 //     S, transposed so that the 128 value columns are the M dimension of every
-//     matrix instruction and S^T, R^T and U~^T = (T~ R)^T are A operands in
-//     TMEM.  S itself stays in the compute warps' registers in FP32 from the
-//     first block to the last: a block's part comes out of TMEM and is added
-//     with one rounding (accumulating in TMEM over all blocks would let the
-//     tensor core's truncated sums drift).
+//     matrix instruction and S^T, R^T and U^T are A operands in TMEM.
+// decay: one kernel, a chain likewise, that forms its operands itself.
+// S itself stays in the state warps' registers in FP32 from the first block to
+// the last: a block's part comes out of TMEM and is added with one rounding
+// (accumulating in TMEM over all blocks would let the tensor core's truncated
+// sums drift).
 //
 // Precision: Q, K and V enter as the bf16 they are.  Every FP32 operand (S, R,
-// U~, T~, G, P) enters as a pair of bf16 values, hi + lo, which leaves 2^-17
+// U, T', G, P, diag(w) V) enters as a pair of bf16 values, hi + lo, which leaves 2^-17
 // of it; products of two pairs drop lo * lo.  Accumulation is FP32.
 //
 // Decays are running products, never quotients or exponentials of sums: a
@@ -55,10 +56,10 @@ __device__ __forceinline__ uint32_t swz(int row, int byte) {     // byte in 0..1
 struct ChunkArgs {
     PrefillArgs p;
     int32_t* first_block;      // [n] index of each request's first block
-    uint8_t* records;          // [max_blocks][H] Rec
+    uint8_t* records;          // [max_blocks][H] DRec
 };
 
-// ------------------------------------------------------------------ prepare
+// ------------------------------------------------------------------ shared
 
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
