@@ -346,7 +346,7 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
  *                   DAMP_EFLAG_TIMEOUT in the pool's status word; the kernel
  *                   then waits (bounded) for its copies in flight and returns,
  *                   so the CUDA context stays usable.
- *   hooks         : 0, or DAMP_HOOK_HOLD_FIRST_ITEM: every CTA of the decode
+ *   hooks         : 0, or bits.  DAMP_HOOK_HOLD_FIRST_ITEM: every CTA of the decode
  *                   step leaves the loads of its first work item unissued, so
  *                   the wait for them runs out; no unit of the call is
  *                   updated or stored and the out rows are left as they were.
@@ -354,9 +354,14 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
  *                   every CTA unissued likewise: a request's state is left as
  *                   it was (quantized pools: as packed again from what the call
  *                   unpacked, zeros for a request without a past).
+ *                   DAMP_HOOK_FAIL_HALF: in the tensor-core kernel that carries
+ *                   a delta-rule prompt's state, one half of the warps (of the
+ *                   key channels; which one goes by the head) takes its first
+ *                   wait of its own as run out, the other half's succeeds.
  * Process-wide, for the launches enqueued after the call.
  */
 #define DAMP_HOOK_HOLD_FIRST_ITEM 1u
+#define DAMP_HOOK_FAIL_HALF 2u
 int damp_set_test_hooks(uint64_t wait_limit_ns, uint32_t hooks);
 
 /*

@@ -32,6 +32,7 @@ DAMP_EFLAG_SLOT_RANGE = 1
 DAMP_EFLAG_TIMEOUT = 2
 DAMP_EFLAG_NONFINITE = 4
 DAMP_HOOK_HOLD_FIRST_ITEM = 1
+DAMP_HOOK_FAIL_HALF = 2
 
 DAMP_FMT_FP32 = 0
 DAMP_FMT_INT8_ROW = 1
@@ -590,7 +591,7 @@ def damp_prefill(pool: int, rule: int, cu_seqlens: torch.Tensor, load_slot: torc
 
 def damp_set_test_hooks(wait_limit_ns: int = 0, hooks: int = 0) -> None:
     """Test hooks of the failure path (process-wide): the bound of the decode
-    step's internal waits (0 = default, 2 s) and DAMP_HOOK_HOLD_FIRST_ITEM."""
+    and prefill's internal waits (0 = default, 2 s) and DAMP_HOOK_* bits."""
     _check(_lib.damp_set_test_hooks(int(wait_limit_ns), int(hooks)), "damp_set_test_hooks")
 
 

@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
     // A group of warps waits by one of them polling and the others at a hardware
     // barrier: 20 polling warps would take the shared-memory pipe from the matrix
     // instructions' operands.  All of the group get the same answer.
-    auto wait_group = [&](bool polls, int i, uint32_t parity, int id, int threads) -> bool {
-        const bool ok = !polls || wait_all(i, parity);
+    auto wait_group = [&](bool polls, int i, uint32_t parity, int id, int threads, bool go = true) -> bool {
+        const bool ok = go && (!polls || wait_all(i, parity));
         return !bar_red_or(id, threads, !ok);
     };
     auto arrive = [&](int i) {
@@ -603,7 +603,19 @@ __global__ void __launch_bounds__(DChain::threads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = has ? in[(size_t)(part * 32 + i) * D + vcol] : 0.f;
         }
-        bool ok = true;
+        // The warps of one half of the channels wait for their own half alone.  A wait that runs out in one
+        // half need not run out in the other, so it is carried (good) to the next wait of all state warps:
+        // they leave the loop together, and no half is left at a barrier that the other will not reach.
+        bool ok = true, good = true;
+        auto wait_half = [&](int i, uint32_t parity) -> bool {
+            const bool polls = quad + (part & 1) == 0;
+            bool fine = !polls || wait_all(i, parity);
+            if (polls && (a.hooks & kHookFailHalf) && part / 2 == (h & 1)) {
+                s_abort = 1;
+                fine = false;
+            }
+            return !bar_red_or(2 + part / 2, X::kWarps * 16, !fine);
+        };
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = c & 1;
             uint8_t* st = sm + (c % X::kStages) * X::stage;
@@ -619,21 +631,22 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             if (live < C) {
                 // rows behind the request's end hold another request's keys and values:
                 // they must not enter the sums over tokens
-                if (!(ok = wait_group(quad + (part & 1) == 0, X::Full + c % X::kStages, (c / X::kStages) & 1,
-                                      2 + part / 2, X::kWarps * 16)))
-                    break;
-                // (a half of the channels by the warps that hand over that half)
-                for (int e = tid % (X::kWarps * 16); e < (C - live) * 8; e += X::kWarps * 16) {
-                    const int at = (live + e / 8) * 128 + (e % 8) * 16;
-                    *reinterpret_cast<uint4*>(st + X::kq + part / 2 * kTile + at) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(st + X::v + part / 2 * kHalf + at) = make_uint4(0, 0, 0, 0);
+                good = good && wait_half(X::Full + c % X::kStages, (c / X::kStages) & 1);
+                if (good) {
+                    // (a half of the channels by the warps that hand over that half)
+                    for (int e = tid % (X::kWarps * 16); e < (C - live) * 8; e += X::kWarps * 16) {
+                        const int at = (live + e / 8) * 128 + (e % 8) * 16;
+                        *reinterpret_cast<uint4*>(st + X::kq + part / 2 * kTile + at) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(st + X::v + part / 2 * kHalf + at) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
             }
             tmem_wait_st();
-            arrive(X::CS + part / 2);
+            if (good) arrive(X::CS + part / 2);
             // ---- R = V - diag(gamma) K S
-            if (!(ok = wait_group(warp == 0, X::Full + c % X::kStages, (c / X::kStages) & 1, 4, X::kWarps * 32)))
+            if (!(ok = wait_group(warp == 0, X::Full + c % X::kStages, (c / X::kStages) & 1, 4, X::kWarps * 32,
+                                  good)))
                 break;
             float v[16];
 #pragma unroll
@@ -684,8 +697,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             tmem_wait_st();
             arrive(X::CU);
             // ---- S <- gamma_C S + the block's part
-            if (!(ok = wait_group(quad + (part & 1) == 0, X::BS + part / 2, ph, 2 + part / 2, X::kWarps * 16)))
-                break;
+            good = wait_half(X::BS + part / 2, ph);
+            if (!good) continue;               // (to the next wait of all, or the last one below)
             tc_fence_after();
             uint32_t y[32];
             tmem_ld32(lanes + X::dS + part * 32, y);
@@ -696,6 +709,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             // every state warp had its values out before that product was issued.
             if (part >= 2 && lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
         }
+        // (all state warps are here, or none: the waits that leave the loop are waits of all)
+        if (ok) ok = !bar_red_or(4, X::kWarps * 32, !good);
         if (ok) {
             float* to = reinterpret_cast<float*>(
                 a.state + (size_t)(a.state_by_slot ? slot : req) * a.state_stride + unit);

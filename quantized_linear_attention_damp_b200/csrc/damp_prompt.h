@@ -5,6 +5,9 @@
 
 namespace damp {
 
+// Test hook of the prefill's chain kernels (DAMP_HOOK_FAIL_HALF).
+constexpr uint32_t kHookFailHalf = 2u;
+
 // Arguments of the batch-plan kernel (damp_plan.cu).
 struct PlanArgs {
     const int32_t* lengths;
@@ -46,7 +49,7 @@ struct PrefillArgs {
     int delta;                 // 1: gated delta rule, 0: decay rule
     int bf16;
     unsigned long long wait_ns;
-    uint32_t hooks;            // test hooks (kHookHoldFirstItem)
+    uint32_t hooks;            // test hooks (kHook...)
     uint8_t* work;             // chunk kernels' workspace
     int max_blocks;
 };
