@@ -328,7 +328,9 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
  * and readouts before their rounding are within about 1e-5 of the recurrence in
  * 64 bits, relative to their norm.  The same call gives the same bits.
  * A wait inside the call that runs out sets DAMP_EFLAG_TIMEOUT; the results of
- * that call are not valid.
+ * that call are not valid.  A (request, head) whose work it kept from being done
+ * keeps its state (quantized pools: as packed again from what the call unpacked,
+ * zeros for a request without a past).
  */
 int damp_prefill_workspace(const damp_pool* pool, int rule, int n, int max_tokens, int in_dtype,
                            size_t* bytes);
@@ -358,10 +360,15 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
  *                   a delta-rule prompt's state, one half of the warps (of the
  *                   key channels; which one goes by the head) takes its first
  *                   wait of its own as run out, the other half's succeeds.
+ *                   DAMP_HOOK_HOLD_FIRST_KERNEL: where damp_prefill's tensor-
+ *                   core form is two kernels (delta rule; decay rule in
+ *                   segments), the first one alone leaves its first loads
+ *                   unissued.
  * Process-wide, for the launches enqueued after the call.
  */
 #define DAMP_HOOK_HOLD_FIRST_ITEM 1u
 #define DAMP_HOOK_FAIL_HALF 2u
+#define DAMP_HOOK_HOLD_FIRST_KERNEL 4u
 int damp_set_test_hooks(uint64_t wait_limit_ns, uint32_t hooks);
 
 /*

@@ -656,7 +656,8 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
 }
 
 int damp_set_test_hooks(uint64_t wait_limit_ns, uint32_t hooks) {
-    if (hooks & ~(DAMP_HOOK_HOLD_FIRST_ITEM | DAMP_HOOK_FAIL_HALF)) return DAMP_ERR_INVALID_ARGUMENT;
+    if (hooks & ~(DAMP_HOOK_HOLD_FIRST_ITEM | DAMP_HOOK_FAIL_HALF | DAMP_HOOK_HOLD_FIRST_KERNEL))
+        return DAMP_ERR_INVALID_ARGUMENT;
     g_wait_ns.store(wait_limit_ns, std::memory_order_relaxed);
     g_hooks.store(hooks, std::memory_order_relaxed);
     return DAMP_OK;

@@ -108,12 +108,15 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 // do not suffice.)
 
 // The record of one (block, head): C x C bf16 matrices with 128-byte rows
-// (K-major, 128-byte swizzle) as the chain's products take them, then gamma_t
-// and gamma_C / gamma_t.
+// (K-major, 128-byte swizzle) as the chain's products take them, gamma_t
+// and gamma_C / gamma_t, and a word that says whether the record is there: a
+// prepare that gives up at a wait leaves kMissing in it, and the chain then
+// leaves its state as it was.
+constexpr uint32_t kThere = 1u, kMissing = 0u;
 struct DRec {
     static constexpr int th = 0, gh = kMat, tl = 2 * kMat, gl = 3 * kMat;   // T' hi, G hi, T' lo, G lo
-    static constexpr int gam = 4 * kMat, w = gam + 4 * C;
-    static constexpr int bytes = w + 4 * C;
+    static constexpr int gam = 4 * kMat, w = gam + 4 * C, there = w + 4 * C;
+    static constexpr int bytes = there + 16;
 };
 
 constexpr int kFA = C + 4;             // floats of a row of A and T
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             fence_mbar_init();
             s_abort = 0;
             const int hq = h / (a.H / a.H_qk);
-            if (!(a.hooks & kHookHoldFirstItem)) {
+            if (!(a.hooks & (kHookHoldFirstItem | kHookHoldFirstKernel))) {
                 mbar_arrive_expect_tx(bar_in, 2 * kTile);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -390,6 +393,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             *reinterpret_cast<uint2*>(img + DRec::tl + swz(r + 8 * i, s * 2)) = lo[i];
         }
     }
+    if (tid == C) *reinterpret_cast<uint32_t*>(img + DRec::there) = kThere;
     if (tid < C) {
         reinterpret_cast<float*>(img + DRec::gam)[tid] = s_ga[tid];
         reinterpret_cast<float*>(img + DRec::w)[tid] = s_w[tid];
@@ -443,10 +447,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             for (int i = 0; i < 2; ++i) mbar_wait_bounded(bar_mma, i, a.wait_ns);
         }
         tmem_free(tm, DPrep::cols);
+        uint8_t* record = ca.records + ((size_t)blk * a.H + h) * DRec::bytes;
         if (s_abort) {
-            if (lane == 0) atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
+            if (lane == 0) {
+                *reinterpret_cast<uint32_t*>(record + DRec::there) = kMissing;
+                atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
+            }
         } else if (elect_one()) {
-            bulk_s2g(ca.records + ((size_t)blk * a.H + h) * DRec::bytes, smem_u32(sm + DPrep::img), DRec::bytes);
+            bulk_s2g(record, smem_u32(sm + DPrep::img), DRec::bytes);
             bulk_commit();
             bulk_wait_read<0>();
         }
@@ -694,10 +702,13 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             tmem_st8(lanes + X::Uh + part * 8, h8);
             tmem_st8(lanes + X::Ul + part * 8, l8);
             const float gc = gam[C - 1];
+            const bool there = *reinterpret_cast<const uint32_t*>(st + X::rec + DRec::there) == kThere;
             tmem_wait_st();
             arrive(X::CU);
             // ---- S <- gamma_C S + the block's part
             good = wait_half(X::BS + part / 2, ph);
+            if (!there) s_abort = 1;           // (for every thread, or none)
+            good = good && there;
             if (!good) continue;               // (to the next wait of all, or the last one below)
             tc_fence_after();
             uint32_t y[32];
@@ -889,6 +900,7 @@ struct SegArgs {
     float* part;               // [n][H][segs][128][128]: state behind segment 0, sums of the others;
                                // the last entry keeps the request's first state
     float* decay;              // [n][H][segs] product of a segment's decays
+    uint32_t* there;           // [n][H][segs] kThere: the first pass left the segment's sum; kMissing: it gave up
 };
 
 template <bool SUM>
@@ -956,7 +968,8 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             fence_mbar_init();
             s_abort = 0;
             // the first blocks are on their way before the rest of the CTA is ready
-            for (int c = a.hooks & kHookHoldFirstItem ? 1 : 0; c < min(nc, X::kStages); ++c) load(c);
+            constexpr uint32_t hold = kHookHoldFirstItem | (SUM ? kHookHoldFirstKernel : 0u);
+            for (int c = a.hooks & hold ? 1 : 0; c < min(nc, X::kStages); ++c) load(c);
         }
         __syncwarp();
     } else if (warp == X::wMma) {
@@ -993,6 +1006,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
         float* parts = sa.part + (size_t)unit * sa.segs * D * D + at;
         const bool has = from >= 0 && from < a.n_slots;
         float S[32];
+        bool ok = true;
         if (seg == 0) {
             // the second pass may find the slot's new state in its place already
             const float* in = !SUM && !last
@@ -1008,6 +1022,9 @@ __global__ void __launch_bounds__(EChain::threads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = SUM ? 0.f : parts[(size_t)i * D];
             if (!SUM)
+                for (int j = 0; j < seg; ++j) ok = ok && sa.there[(size_t)unit * sa.segs + j] == kThere;
+            if (!ok) s_abort = 1;              // (for every thread, or none; the state stays as it was)
+            if (!SUM)
                 for (int j = 1; j < seg; ++j) {
                     const float g = sa.decay[(size_t)unit * sa.segs + j];
 #pragma unroll
@@ -1016,8 +1033,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
                 }
         }
         float total = 1.f;
-        bool ok = true;
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
             if (!SUM) {
                 // ---- the state before block c as a pair
@@ -1048,6 +1064,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             }
             total *= gc;
         }
+        if (SUM && tid == 0) sa.there[(size_t)unit * sa.segs + seg] = ok ? kThere : kMissing;
         if (ok) {
             if (SUM) {
 #pragma unroll
@@ -1391,7 +1408,7 @@ bool prefill_chunk_fits(int d_k, int d_v, int bf16) { return bf16 && d_k == D &&
 size_t prefill_chunk_bytes(int n, int H, int max_tokens, int max_blocks, int delta) {
     if (delta) return first_block_bytes(n) + (size_t)max_blocks * H * DRec::bytes;
     const int segs = decay_segments(n, H, max_tokens, kSms);
-    return segs == 1 ? 0 : (size_t)n * H * segs * (D * D + 1) * 4;
+    return segs == 1 ? 0 : (size_t)n * H * segs * (D * D + 2) * 4;
 }
 
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
@@ -1403,8 +1420,10 @@ cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ChunkArgs ca{a, nullptr, nullptr};
     if (!a.delta) {
-        SegArgs sa{decay_segments(a.n, a.H, a.max_tokens, kSms), reinterpret_cast<float*>(a.work), nullptr};
+        SegArgs sa{decay_segments(a.n, a.H, a.max_tokens, kSms), reinterpret_cast<float*>(a.work), nullptr,
+                   nullptr};
         sa.decay = sa.part + (size_t)a.n * a.H * sa.segs * D * D;
+        sa.there = reinterpret_cast<uint32_t*>(sa.decay + (size_t)a.n * a.H * sa.segs);
         const int grid = a.n * a.H * sa.segs;
         if (sa.segs > 1) {
             decay_chain_kernel<true><<<grid, EChain::threads, EChain::bytes, s>>>(ca, sa, mq, mk, mv);

@@ -5,8 +5,9 @@
 
 namespace damp {
 
-// Test hook of the prefill's chain kernels (DAMP_HOOK_FAIL_HALF).
+// Test hooks of the prefill's block kernels (DAMP_HOOK_FAIL_HALF, DAMP_HOOK_HOLD_FIRST_KERNEL).
 constexpr uint32_t kHookFailHalf = 2u;
+constexpr uint32_t kHookHoldFirstKernel = 4u;
 
 // Arguments of the batch-plan kernel (damp_plan.cu).
 struct PlanArgs {

@@ -69,3 +69,26 @@ def test_one_half_of_the_state_warps_runs_out(L, H):
 def test_the_decay_rule_has_no_halves():
     first, after, flags = call_under(D.DAMP_HOOK_FAIL_HALF, "decay", [150, 64], 2)
     assert flags == 0 and not torch.equal(after, first)
+
+
+@pytest.mark.parametrize("fmt", ["fp32", "mixed"])
+@pytest.mark.parametrize("rule,lengths", [("delta", [40, 64, 200]), ("decay", [1200]), ("decay", [2000, 300, 900])])
+def test_the_first_of_two_kernels_runs_out(rule, lengths, fmt):
+    """The second kernel leaves the states alone when what the first one was to hand over is not there
+    (the workspace holds NaN).  The decay rule has two kernels where it cuts requests into segments; the
+    one of 300 tokens is a single segment, which does not need the first kernel."""
+    H, d, n = 2, 128, len(lengths)
+    first, after, flags = call_under(D.DAMP_HOOK_HOLD_FIRST_KERNEL, rule, lengths, H, fmt)
+    assert flags == D.DAMP_EFLAG_TIMEOUT
+    rows = np.stack([np.arange(h, 64 + h, 3) for h in range(H)]) if fmt == "mixed" else None
+    pool = D.DampPool(fmt, n + 1, H, d, rows)
+    values = [torch.empty(n + 1, H, d, d, device="cuda") for _ in range(2)]
+    for slots, out in zip((first, after), values):
+        pool.slots().copy_(slots)
+        pool.unpack(i32(list(range(n + 1))), out)
+    pool.close()
+    # (a quantized pool's values are packed again: half a code's step, 1/127 of the row's largest value)
+    step = 0.0 if fmt == "fp32" else values[0].abs().amax(dim=3, keepdim=True) / 127
+    kept = ((values[0] - values[1]).abs() <= 0.51 * step).flatten(1).all(dim=1)
+    assert torch.isfinite(values[1]).all()
+    assert kept.sum() >= n + 1 - (300 in lengths), kept
