@@ -24,9 +24,16 @@
 // (accumulating in TMEM over all blocks would let the tensor core's truncated
 // sums drift).
 //
-// Precision: Q, K and V enter as the bf16 they are.  Every FP32 operand (S, R,
-// U, T', G, P, diag(w) V) enters as a pair of bf16 values, hi + lo, which leaves 2^-17
-// of it; products of two pairs drop lo * lo.  Accumulation is FP32.
+// Precision: Q, K and V enter as the bf16 they are, accumulation is FP32.  The
+// delta rule's FP32 operands of whatever a state is made of (S in K S, T' and R
+// in T' R, diag(w) U) enter as three bf16 terms, which hold all their bits; the
+// product of two such keeps every pair of terms down to 2^-18 (6 of 9).  Pairs
+// are not enough there: with equal keys T' alternates in sign, T' R cancels, and
+// what the pairs had lost came to 1e-3 of the state (beta |k|^2 = 1.9, where the
+// recurrence is stable and FP32 sums of the same form keep 2e-5).
+// What only a readout is made of (P, G, R in G R, S in Q S), and the decay rule's
+// diag(w) V, enters as a pair, hi + mid, which leaves 2^-17 of it: a readout is
+// rounded to bf16 (2^-8) afterwards.
 //
 // Decays are running products, never quotients or exponentials of sums: a
 // decay of zero inside a block, or products that underflow, need no care.
@@ -114,8 +121,9 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 // leaves its state as it was.
 constexpr uint32_t kThere = 1u, kMissing = 0u;
 struct DRec {
-    static constexpr int th = 0, gh = kMat, tl = 2 * kMat, gl = 3 * kMat;   // T' hi, G hi, T' lo, G lo
-    static constexpr int gam = 4 * kMat, w = gam + 4 * C, there = w + 4 * C;
+    static constexpr int th = 0, tm = kMat, tl = 2 * kMat;   // T' hi, mid, lo
+    static constexpr int gh = 3 * kMat, gm = 4 * kMat;       // G hi, mid
+    static constexpr int gam = 5 * kMat, w = gam + 4 * C, there = w + 4 * C;
     static constexpr int bytes = there + 16;
 };
 
@@ -124,9 +132,10 @@ struct DPrep {
     static constexpr int qk = 0;                       // Q0 K0 Q1 K1: halves of 64 channels
     static constexpr int a = 0, t = C * kFA * 4;       // over Q and K
     static constexpr int img = 0;                      // over A and T
-    static constexpr int vec = 2 * C * kFA * 4;        // alpha, beta, gamma, w
+    static constexpr int vec = DRec::bytes > 2 * C * kFA * 4 ? DRec::bytes : 2 * C * kFA * 4;
+                                                       // alpha, beta, gamma, w
     static constexpr int bytes = vec + 4 * C * 4 + 1024;
-    static_assert(2 * kTile <= vec && DRec::bytes <= vec, "Q and K, and the record, fit over A and T");
+    static_assert(2 * kTile <= vec && vec % 16 == 0, "Q and K fit over A and T");
     // TMEM: [Q; K] K^T, then P hi, lo (32 columns each); G
     static constexpr uint32_t tQK = 0, tP = 0, tG = 64, cols = 128;
 };
@@ -372,24 +381,27 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         }
     }
     __syncthreads();
-    // ---- T' = T diag(beta) as bf16 pairs in the record's image (over A and T: through registers).
+    // ---- T' = T diag(beta) as three bf16 terms in the record's image (over A and T: through registers).
     // Behind the request's end beta is zero, so those columns vanish, and A has no such rows.
     uint8_t* img = sm + DPrep::img;
     {
         const int s = (tid & 15) * 4, r = tid >> 4;       // 4 columns, rows r, r + 8, ...
         const float4 be = *reinterpret_cast<const float4*>(s_be + s);
-        uint2 hi[C / 8], lo[C / 8];
+        uint2 hi[C / 8], mid[C / 8], lo[C / 8];
 #pragma unroll
         for (int i = 0; i < C / 8; ++i) {
             const int t = r + 8 * i;
             const float4 tv = *reinterpret_cast<const float4*>(&s_t[t * kFA + s]);
-            split_bf16(s <= t ? tv.x * be.x : 0.f, s + 1 <= t ? tv.y * be.y : 0.f, hi[i].x, lo[i].x);
-            split_bf16(s + 2 <= t ? tv.z * be.z : 0.f, s + 3 <= t ? tv.w * be.w : 0.f, hi[i].y, lo[i].y);
+            split3_bf16(make_float2(s <= t ? tv.x * be.x : 0.f, s + 1 <= t ? tv.y * be.y : 0.f), hi[i].x, mid[i].x,
+                        lo[i].x);
+            split3_bf16(make_float2(s + 2 <= t ? tv.z * be.z : 0.f, s + 3 <= t ? tv.w * be.w : 0.f), hi[i].y,
+                        mid[i].y, lo[i].y);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < C / 8; ++i) {
             *reinterpret_cast<uint2*>(img + DRec::th + swz(r + 8 * i, s * 2)) = hi[i];
+            *reinterpret_cast<uint2*>(img + DRec::tm + swz(r + 8 * i, s * 2)) = mid[i];
             *reinterpret_cast<uint2*>(img + DRec::tl + swz(r + 8 * i, s * 2)) = lo[i];
         }
     }
@@ -400,7 +412,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     fence_proxy_async_smem();
     __syncthreads();
-    // ---- G = P T': hi * hi, lo * hi, hi * lo (rows 64..127 of M are not used)
+    // ---- G = P T': hi * hi, mid * hi, hi * mid (rows 64..127 of M are not used)
     if (warp == 0) {
         tc_fence_after();
         if (elect_one()) {
@@ -408,7 +420,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 #pragma unroll
             for (int ks = 0; ks < 12; ++ks)
                 mma_ts(tm + DPrep::tG, tm + DPrep::tP + 8 * (ks & 7),
-                       desc_mn_major(base + DPrep::img + (ks < 8 ? DRec::th : DRec::tl) + (ks & 3) * 2048, kMat), id,
+                       desc_mn_major(base + DPrep::img + (ks < 8 ? DRec::th : DRec::tm) + (ks & 3) * 2048, kMat), id,
                        ks > 0);
             tc_commit(bar_mma);
         }
@@ -430,7 +442,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 split_bf16(__uint_as_float(y[8 * j + 6]), __uint_as_float(y[8 * j + 7]), hi.w, lo.w);
                 const uint32_t at = swz(t, part * 64 + j * 16);
                 *reinterpret_cast<uint4*>(img + DRec::gh + at) = hi;
-                *reinterpret_cast<uint4*>(img + DRec::gl + at) = lo;
+                *reinterpret_cast<uint4*>(img + DRec::gm + at) = lo;
             }
         }
     }
@@ -485,13 +497,14 @@ struct DChain {
     static constexpr int bytes = bar + 256 + 1024;
     // TMEM columns
     static constexpr uint32_t dS = 0;       // the block's part of S^T, FP32 [128 v][128 k]
-    static constexpr uint32_t Sh = 128;     // S^T hi, lo (64 columns each)
-    static constexpr uint32_t Rh = 0;       // R^T hi, lo (32 each), while dS is not needed
-    static constexpr uint32_t Uh = 160;     // (diag(w) U)^T hi, over S's hi of the channels' second half,
-    static constexpr uint32_t Ul = 224;     // and lo over its lo: the first half's next pair is written
-                                            // while the second half's product still reads U
-    static constexpr uint32_t KQ = 256;     // (K S)^T, (Q S)^T, FP32 [128][64] each
-    static constexpr uint32_t UO = 384;     // U^T, (G R)^T
+    static constexpr uint32_t S = 128;      // S^T hi, mid, lo (64 columns each)
+    static constexpr uint32_t R = 0;        // R^T hi, mid, lo (32 each), while dS is not needed
+    static constexpr uint32_t U = 160;      // (diag(w) U)^T hi, mid, lo (64 apart), over S's terms of the channels'
+                                            // second half: the first half's next terms are written while the
+                                            // second half's product still reads U
+    static constexpr uint32_t KS = 320;     // (K S)^T, FP32 [128][64], then U^T in its place: R is formed, and
+                                            // K S with it read, before T' R is issued
+    static constexpr uint32_t QS = 384, GR = 448;   // (Q S)^T, (G R)^T
     // Barriers.  B*: a product is done (KS; U; Q S and G R; S's two halves).  C*: the state
     // warps have left an operand in TMEM (S's halves, R, U); CO: the readout is out of TMEM.
     enum { Full = 0, Empty = kStages, BK = 2 * kStages, BU, BO, BS, CS = BS + 2, CR = CS + 2, CU, CO, Drain };
@@ -629,12 +642,17 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             uint8_t* st = sm + (c % X::kStages) * X::stage;
             const float* gam = reinterpret_cast<const float*>(st + X::rec + DRec::gam);
             const float* w = reinterpret_cast<const float*>(st + X::rec + DRec::w);
-            // ---- the state before block c as a pair
-            uint32_t hi[16], lo[16];
+            // ---- the state before block c as three terms
+            uint32_t h8[8], m8[8], l8[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) split_bf16(S[2 * i], S[2 * i + 1], hi[i], lo[i]);
-            tmem_st16(lanes + X::Sh + part * 16, hi);
-            tmem_st16(lanes + X::Sh + 64 + part * 16, lo);
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    split3_bf16(make_float2(S[16 * j + 2 * i], S[16 * j + 2 * i + 1]), h8[i], m8[i], l8[i]);
+                tmem_st8(lanes + X::S + part * 16 + j * 8, h8);
+                tmem_st8(lanes + X::S + 64 + part * 16 + j * 8, m8);
+                tmem_st8(lanes + X::S + 128 + part * 16 + j * 8, l8);
+            }
             const int live = min(C, len - c * C);         // tokens of block c
             if (live < C) {
                 // rows behind the request's end hold another request's keys and values:
@@ -664,12 +682,12 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                     st + X::v + (vcol >> 6) * kHalf + swz(t, (vcol & 63) * 2));
                 v[i] = __uint_as_float((uint32_t)b << 16);
             }
-            uint32_t x[16], h8[8], l8[8];
+            uint32_t x[16];
             // (the decays of R behind the wait, the factors of U ahead of theirs, as measured: with both
             // ahead a thread's registers do not suffice, 450 us against 418 for 8192 tokens x 32 heads)
             if (!(ok = wait_group(warp == 0, X::BK, ph, 4, X::kWarps * 32))) break;
             tc_fence_after();
-            tmem_ld16(lanes + X::KQ + part * 16, x);
+            tmem_ld16(lanes + X::KS + part * 16, x);
             float g[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -679,13 +697,15 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                split_bf16(__fmaf_rn(-g[2 * i], __uint_as_float(x[2 * i]), v[2 * i]),
-                           __fmaf_rn(-g[2 * i + 1], __uint_as_float(x[2 * i + 1]), v[2 * i + 1]), h8[i], l8[i]);
-            tmem_st8(lanes + X::Rh + part * 8, h8);
-            tmem_st8(lanes + X::Rh + 32 + part * 8, l8);
+                split3_bf16(make_float2(__fmaf_rn(-g[2 * i], __uint_as_float(x[2 * i]), v[2 * i]),
+                                        __fmaf_rn(-g[2 * i + 1], __uint_as_float(x[2 * i + 1]), v[2 * i + 1])),
+                            h8[i], m8[i], l8[i]);
+            tmem_st8(lanes + X::R + part * 8, h8);
+            tmem_st8(lanes + X::R + 32 + part * 8, m8);
+            tmem_st8(lanes + X::R + 64 + part * 8, l8);
             tmem_wait_st();
             arrive(X::CR);
-            // ---- diag(w) U as a pair
+            // ---- diag(w) U as three terms
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 f = reinterpret_cast<const float4*>(w + part * 16)[i];
@@ -693,14 +713,16 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             }
             if (!(ok = wait_group(warp == 0, X::BU, ph, 4, X::kWarps * 32))) break;
             tc_fence_after();
-            tmem_ld16(lanes + X::UO + part * 16, x);
+            tmem_ld16(lanes + X::KS + part * 16, x);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                split_bf16(g[2 * i] * __uint_as_float(x[2 * i]), g[2 * i + 1] * __uint_as_float(x[2 * i + 1]), h8[i],
-                           l8[i]);
-            tmem_st8(lanes + X::Uh + part * 8, h8);
-            tmem_st8(lanes + X::Ul + part * 8, l8);
+                split3_bf16(make_float2(g[2 * i] * __uint_as_float(x[2 * i]),
+                                        g[2 * i + 1] * __uint_as_float(x[2 * i + 1])),
+                            h8[i], m8[i], l8[i]);
+            tmem_st8(lanes + X::U + part * 8, h8);
+            tmem_st8(lanes + X::U + 64 + part * 8, m8);
+            tmem_st8(lanes + X::U + 128 + part * 8, l8);
             const float gc = gam[C - 1];
             const bool there = *reinterpret_cast<const uint32_t*>(st + X::rec + DRec::there) == kThere;
             tmem_wait_st();
@@ -740,8 +762,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
 #pragma unroll 1
             for (int part = 0; part < 4; ++part) {
                 uint32_t o1[16], o2[16];
-                tmem_ld16(lanes + X::KQ + 64 + part * 16, o1);
-                tmem_ld16(lanes + X::UO + 64 + part * 16, o2);
+                tmem_ld16(lanes + X::QS + part * 16, o1);
+                tmem_ld16(lanes + X::GR + part * 16, o2);
                 float2 gt[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) gt[i] = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
@@ -792,7 +814,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             const uint32_t ph = c & 1;
             if (!wait_all(X::Full + c % X::kStages, (c / X::kStages) & 1)) break;
             if (c > 0 && !wait_all(X::CO, ph ^ 1)) break;
-            // (K S)^T, the channels' first half as soon as it is there; each hi, then lo
+            // (K S)^T, the channels' first half as soon as it is there.  Small terms go first here and
+            // below: the tensor core truncates its sums, the less the smaller they are.
             bool ok = true;
 #pragma unroll
             for (int half = 0; half < 2 && ok; ++half) {
@@ -800,34 +823,35 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tm + X::KQ, tm + X::Sh + (ks >> 2) * 64 + half * 32 + (ks & 3) * 8,
+                    for (int ks = 0; ks < 12; ++ks)
+                        mma_ts(tm + X::KS, tm + X::S + (2 - (ks >> 2)) * 64 + half * 32 + (ks & 3) * 8,
                                desc_k_major(st + X::kq + half * kTile + (ks & 3) * 32), idk, half + ks > 0);
                     if (half == 1) {
                         tc_commit(bar(X::BK));
-                        // (Q S)^T, while the state warps work on R
+                        // (Q S)^T, hi and mid, while the state warps work on R
 #pragma unroll
                         for (int ks = 0; ks < 16; ++ks)
-                            mma_ts(tm + X::KQ + 64, tm + X::Sh + 8 * ks,
+                            mma_ts(tm + X::QS, tm + X::S + 8 * ks,
                                    desc_k_major(st + X::kq + ((ks >> 2) & 1) * kTile + kHalf + (ks & 3) * 32),
                                    idk, ks > 0);
                     }
                 }
             }
             if (!ok) break;
-            // U^T = (T' R)^T, then (G R)^T: hi * hi, lo * hi, hi * lo
+            // U^T = (T' R)^T in six products of terms, then (G R)^T: hi * hi, mid * hi, hi * mid
             if (!wait_all(X::CR, ph)) break;
             tc_fence_after();
             if (elect_one()) {
+                constexpr int r[6] = {2, 1, 0, 1, 0, 0}, t[6] = {0, 1, 2, 0, 1, 0};    // terms of R and of T'
 #pragma unroll
-                for (int ks = 0; ks < 12; ++ks)
-                    mma_ts(tm + X::UO, tm + X::Rh + 8 * (ks & 7),
-                           desc_k_major(rec + (ks < 8 ? DRec::th : DRec::tl) + (ks & 3) * 32), idk, ks > 0);
+                for (int ks = 0; ks < 24; ++ks)
+                    mma_ts(tm + X::KS, tm + X::R + r[ks >> 2] * 32 + 8 * (ks & 3),
+                           desc_k_major(rec + t[ks >> 2] * kMat + (ks & 3) * 32), idk, ks > 0);
                 tc_commit(bar(X::BU));
 #pragma unroll
                 for (int ks = 0; ks < 12; ++ks)
-                    mma_ts(tm + X::UO + 64, tm + X::Rh + 8 * (ks & 7),
-                           desc_k_major(rec + (ks < 8 ? DRec::gh : DRec::gl) + (ks & 3) * 32), idk, ks > 0);
+                    mma_ts(tm + X::GR, tm + X::R + 8 * (ks & 7),
+                           desc_k_major(rec + (ks < 8 ? DRec::gh : DRec::gm) + (ks & 3) * 32), idk, ks > 0);
                 tc_commit(bar(X::BO));
             }
             // the block's part of S^T, by halves of its channels
@@ -837,8 +861,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tm + X::dS + half * 64, tm + (ks < 4 ? X::Uh : X::Ul) + 8 * (ks & 3),
+                    for (int ks = 0; ks < 12; ++ks)
+                        mma_ts(tm + X::dS + half * 64, tm + X::U + (2 - (ks >> 2)) * 64 + 8 * (ks & 3),
                                desc_mn_major(st + X::kq + half * kTile + (ks & 3) * 2048, kTile), idmn, ks > 0);
                     tc_commit(bar(X::BS + half));
                 }

@@ -196,5 +196,11 @@ __device__ __forceinline__ void split_bf16(float2 x, uint32_t& hi, uint32_t& lo)
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
     split_bf16(make_float2(a, b), hi, lo);
 }
+// Three terms hold all 24 bits: x = hi + mid + lo (down to bf16's smallest value).
+__device__ __forceinline__ void split3_bf16(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack_bf16(x.x, x.y);
+    const float2 h = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    split_bf16(__ffma2_rn(h, make_float2(-1.f, -1.f), x), mid, lo);
+}
 
 }  // namespace damp
