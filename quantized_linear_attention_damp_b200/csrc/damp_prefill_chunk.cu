@@ -1124,6 +1124,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             }
             // the block before last has used this pair up
             if (!wait_group(c >= 2 && warp == lead, X::BD + buf, ((c >> 1) - 1) & 1, kId, kN)) return false;
+            tc_fence_after();
             const float* w = ring(c) + 2 * C;
 #pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {   // 16 value columns (TMEM lanes) each, transposed by ldmatrix
