@@ -10,10 +10,9 @@
 //                S <- gamma_C S + K^T diag(gamma_C / gamma) U
 //   decay rule:  the same with U = V.
 // delta: two kernels.
-//   prepare (one CTA per block and head, no order between blocks): everything
-//     that does not depend on S.  T' = (I + A)^-1 diag(beta) and
-//     G = (Q K^T o Gamma) T', so that with R = V - diag(gamma) K S and
-//     U = T' R:  O = diag(gamma) Q S + G R and
+//   prepare (one CTA per block and head, no order between blocks): what does not
+//     depend on S: T' = (I + A)^-1 diag(beta) and P = Q K^T o Gamma, so that with
+//     R = V - diag(gamma) K S and U = T' R:  O = diag(gamma) Q S + P U and
 //     S <- gamma_C S + K^T diag(gamma_C / gamma) U.
 //   chain (one CTA per request and head, blocks in order): the products with
 //     S, transposed so that the 128 value columns are the M dimension of every
@@ -31,9 +30,10 @@
 // are not enough there: with equal keys T' alternates in sign, T' R cancels, and
 // what the pairs had lost came to 1e-3 of the state (beta |k|^2 = 1.9, where the
 // recurrence is stable and FP32 sums of the same form keep 2e-5).
-// What only a readout is made of (P, G, R in G R, S in Q S), and the decay rule's
+// What only a readout is made of (P and U in P U, S in Q S), and the decay rule's
 // diag(w) V, enters as a pair, hi + mid, which leaves 2^-17 of it: a readout is
-// rounded to bf16 (2^-8) afterwards.
+// rounded to bf16 (2^-8) afterwards.  (As G R with G = P T', which needs no U, the
+// readout would cancel as T' R does: 1.4e-3 of it lost with equal keys.)
 //
 // Decays are running products, never quotients or exponentials of sums: a
 // decay of zero inside a block, or products that underflow, need no care.
@@ -101,18 +101,12 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 
 // ------------------------------------------------------------------ delta: prepare
 //
-// 128 threads a (block, head), four CTAs an SM (TMEM: 128 columns each): the
-// steps are short and each waits for the one before, so it is the number of
-// resident CTAs that keeps the SM busy.  [Q; K] K^T is one tensor-core product
-// of 128 rows; a thread then has one row of Q K^T (warps 0, 1) or K K^T (warps
-// 2, 3) and multiplies the decays up along it.  P = Q K^T o Gamma goes back to
-// TMEM as the A operand of G = P T'.  The inverse is FP32 arithmetic of the
-// ordinary kind: an error of it is an error of the state.  Q and K share their
-// 32 KB with A and T (FP32) and then with the finished record.
-// (4096 units: 83 us; with products by mma.sync, staged by the threads, 97.
-// With P handed over in shared memory, so that 64 columns of TMEM are enough:
-// no faster with 5 CTAs an SM than with 4, slower with 6, whose 80 registers
-// do not suffice.)
+// 128 threads a (block, head), four CTAs an SM: the steps are short and each waits
+// for the one before, so it is the number of resident CTAs that keeps the SM busy.
+// [Q; K] K^T is one tensor-core product of 128 rows; a thread then has one row of
+// Q K^T (warps 0, 1) or K K^T (warps 2, 3) and multiplies the decays up along it.
+// The inverse is FP32 arithmetic of the ordinary kind: an error of it is an error
+// of the state.  Q and K share their 32 KB with A and T (FP32) and then with T'.
 
 // The record of one (block, head): C x C bf16 matrices with 128-byte rows
 // (K-major, 128-byte swizzle) as the chain's products take them, gamma_t
@@ -122,7 +116,7 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 constexpr uint32_t kThere = 1u, kMissing = 0u;
 struct DRec {
     static constexpr int th = 0, tm = kMat, tl = 2 * kMat;   // T' hi, mid, lo
-    static constexpr int gh = 3 * kMat, gm = 4 * kMat;       // G hi, mid
+    static constexpr int ph = 3 * kMat, pm = 4 * kMat;       // P hi, mid
     static constexpr int gam = 5 * kMat, w = gam + 4 * C, there = w + 4 * C;
     static constexpr int bytes = there + 16;
 };
@@ -131,13 +125,12 @@ constexpr int kFA = C + 4;             // floats of a row of A and T
 struct DPrep {
     static constexpr int qk = 0;                       // Q0 K0 Q1 K1: halves of 64 channels
     static constexpr int a = 0, t = C * kFA * 4;       // over Q and K
-    static constexpr int img = 0;                      // over A and T
-    static constexpr int vec = DRec::bytes > 2 * C * kFA * 4 ? DRec::bytes : 2 * C * kFA * 4;
-                                                       // alpha, beta, gamma, w
-    static constexpr int bytes = vec + 4 * C * 4 + 1024;
-    static_assert(2 * kTile <= vec && vec % 16 == 0, "Q and K fit over A and T");
-    // TMEM: [Q; K] K^T, then P hi, lo (32 columns each); G
-    static constexpr uint32_t tQK = 0, tP = 0, tG = 64, cols = 128;
+    static constexpr int img = 0;                      // T', over A and T
+    static constexpr int end = 2 * C * kFA * 4;        // the record from P on
+    static constexpr int vec = end + DRec::bytes - DRec::ph;           // alpha, beta
+    static constexpr int bytes = vec + 2 * C * 4 + 1024;
+    static_assert(2 * kTile <= end && DRec::ph <= end && vec % 16 == 0, "Q and K, and T', fit over A and T");
+    static constexpr uint32_t cols = 64;               // TMEM: [Q; K] K^T
 };
 
 __global__ void __launch_bounds__(kPrepThreads, 4)
@@ -147,7 +140,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     extern __shared__ __align__(1024) uint8_t sm_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    __shared__ __align__(8) uint64_t s_bar[2];
+    __shared__ __align__(8) uint64_t s_bar[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // heads of a block run side by side: their rows of Q and K are neighbours in memory
     const int blk = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -161,14 +154,17 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     uint8_t* sm = sm_raw + (base - smem_u32(sm_raw));
     float* s_al = reinterpret_cast<float*>(sm + DPrep::vec);
     float* s_be = s_al + C;
-    float* s_ga = s_al + 2 * C;
-    float* s_w = s_al + 3 * C;
-    const uint32_t bar_in = smem_u32(&s_bar[0]), bar_mma = smem_u32(&s_bar[1]);
+    uint8_t* img = sm + DPrep::img;
+    uint8_t* img2 = sm + DPrep::end - DRec::ph;        // the record's places from P on
+    float* s_ga = reinterpret_cast<float*>(img2 + DRec::gam);
+    float* s_w = reinterpret_cast<float*>(img2 + DRec::w);
+    const uint32_t bar_in = smem_u32(&s_bar[0]), bar_mma = smem_u32(&s_bar[1]), bar_drain = smem_u32(&s_bar[2]);
 
     if (warp == 0) {
         if (elect_one()) {
             mbar_init(bar_in, 1);
             mbar_init(bar_mma, 1);
+            mbar_init(bar_drain, 1);
             fence_mbar_init();
             s_abort = 0;
             const int hq = h / (a.H / a.H_qk);
@@ -229,7 +225,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 const uint32_t at = base + DPrep::qk + (ks >> 2) * kTile + (ks & 3) * 32;
-                mma_ss(tm + DPrep::tQK, desc_k_major(at), desc_k_major(at + kHalf), id, ks > 0);
+                mma_ss(tm, desc_k_major(at), desc_k_major(at + kHalf), id, ks > 0);
             }
             tc_commit(bar_mma);
         }
@@ -242,47 +238,54 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     float* s_t = reinterpret_cast<float*>(sm + DPrep::t);
     const int r0 = warp * 16;
     if (fine) {
-        // ---- row t of P (to TMEM as a pair) or of A = diag(beta) K K^T o Gamma below the diagonal
+        // ---- row t of P (as a pair) or of A = diag(beta) K K^T o Gamma below the diagonal
         const int t = (warp & 1) * 32 + lane;
         const bool is_p = warp < 2;
         // gamma_t / gamma_s from s = t down (times beta_t for A), zero above; rows of P behind the
         // request's end are used by no one
         const float first = is_p ? 1.f : s_be[t];
         float x = 0.f, above = 1.f;                // above: alpha_{s + 1}
-        uint32_t hi[2][16] = {}, lo[2][16] = {};
 #pragma unroll
         for (int part = 1; part >= 0; --part) {
-            if (part > (warp & 1)) continue;       // above the diagonal: P stays zero, A is not read
+            if (part > (warp & 1)) {               // above the diagonal: P is zero, A is not read
+                if (is_p)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        *reinterpret_cast<uint4*>(img2 + DRec::ph + swz(t, part * 64 + j * 16)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(img2 + DRec::pm + swz(t, part * 64 + j * 16)) = make_uint4(0, 0, 0, 0);
+                    }
+                continue;
+            }
             uint32_t y[32];
-            tmem_ld32(lanes + DPrep::tQK + part * 32, y);
+            tmem_ld32(lanes + part * 32, y);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 7; j >= 0; --j) {
-                const float4 av = *reinterpret_cast<const float4*>(s_al + part * 32 + j * 4);
-                const float as[4] = {av.x, av.y, av.z, av.w};
-                float f[4];
+            for (int j = 3; j >= 0; --j) {
+                const float4 a1 = *reinterpret_cast<const float4*>(s_al + part * 32 + j * 8 + 4);
+                const float4 a0 = *reinterpret_cast<const float4*>(s_al + part * 32 + j * 8);
+                const float as[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                float f[8];
 #pragma unroll
-                for (int i = 3; i >= 0; --i) {
+                for (int i = 7; i >= 0; --i) {
                     const float z = x * above;
-                    x = part * 32 + j * 4 + i == t ? first : z;
+                    x = part * 32 + j * 8 + i == t ? first : z;
                     above = as[i];
-                    f[i] = (is_p ? x : z) * __uint_as_float(y[j * 4 + i]);     // A: zero on the diagonal
+                    f[i] = (is_p ? x : z) * __uint_as_float(y[j * 8 + i]);     // A: zero on the diagonal
                 }
                 if (is_p) {
-                    split_bf16(f[0], f[1], hi[part][2 * j], lo[part][2 * j]);
-                    split_bf16(f[2], f[3], hi[part][2 * j + 1], lo[part][2 * j + 1]);
+                    uint4 hi, mid;
+                    split_bf16(f[0], f[1], hi.x, mid.x);
+                    split_bf16(f[2], f[3], hi.y, mid.y);
+                    split_bf16(f[4], f[5], hi.z, mid.z);
+                    split_bf16(f[6], f[7], hi.w, mid.w);
+                    *reinterpret_cast<uint4*>(img2 + DRec::ph + swz(t, part * 64 + j * 16)) = hi;
+                    *reinterpret_cast<uint4*>(img2 + DRec::pm + swz(t, part * 64 + j * 16)) = mid;
                 } else {
-                    *reinterpret_cast<float4*>(s_a + t * kFA + part * 32 + j * 4) = make_float4(f[0], f[1], f[2], f[3]);
+                    float4* to = reinterpret_cast<float4*>(s_a + t * kFA + part * 32 + j * 8);
+                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
                 }
             }
-        }
-        if (is_p) {
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                tmem_st16(lanes + DPrep::tP + part * 16, hi[part]);
-                tmem_st16(lanes + DPrep::tP + 32 + part * 16, lo[part]);
-            }
-            tmem_wait_st();
         }
     }
     tc_fence_before();
@@ -383,7 +386,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     __syncthreads();
     // ---- T' = T diag(beta) as three bf16 terms in the record's image (over A and T: through registers).
     // Behind the request's end beta is zero, so those columns vanish, and A has no such rows.
-    uint8_t* img = sm + DPrep::img;
     {
         const int s = (tid & 15) * 4, r = tid >> 4;       // 4 columns, rows r, r + 8, ...
         const float4 be = *reinterpret_cast<const float4*>(s_be + s);
@@ -405,47 +407,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             *reinterpret_cast<uint2*>(img + DRec::tl + swz(r + 8 * i, s * 2)) = lo[i];
         }
     }
-    if (tid == C) *reinterpret_cast<uint32_t*>(img + DRec::there) = kThere;
-    if (tid < C) {
-        reinterpret_cast<float*>(img + DRec::gam)[tid] = s_ga[tid];
-        reinterpret_cast<float*>(img + DRec::w)[tid] = s_w[tid];
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    // ---- G = P T': hi * hi, mid * hi, hi * mid (rows 64..127 of M are not used)
-    if (warp == 0) {
-        tc_fence_after();
-        if (elect_one()) {
-            constexpr uint32_t id = mma_idesc(128, 64, false, true);
-#pragma unroll
-            for (int ks = 0; ks < 12; ++ks)
-                mma_ts(tm + DPrep::tG, tm + DPrep::tP + 8 * (ks & 7),
-                       desc_mn_major(base + DPrep::img + (ks < 8 ? DRec::th : DRec::tm) + (ks & 3) * 2048, kMat), id,
-                       ks > 0);
-            tc_commit(bar_mma);
-        }
-    }
-    if (warp < 2 && __all_sync(0xffffffffu, bounded_wait(bar_mma, 1, a.wait_ns, &s_abort, false))) {
-        tc_fence_after();
-        const int t = warp * 32 + lane;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            uint32_t y[32];
-            tmem_ld32(lanes + DPrep::tG + part * 32, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4 hi, lo;
-                split_bf16(__uint_as_float(y[8 * j]), __uint_as_float(y[8 * j + 1]), hi.x, lo.x);
-                split_bf16(__uint_as_float(y[8 * j + 2]), __uint_as_float(y[8 * j + 3]), hi.y, lo.y);
-                split_bf16(__uint_as_float(y[8 * j + 4]), __uint_as_float(y[8 * j + 5]), hi.z, lo.z);
-                split_bf16(__uint_as_float(y[8 * j + 6]), __uint_as_float(y[8 * j + 7]), hi.w, lo.w);
-                const uint32_t at = swz(t, part * 64 + j * 16);
-                *reinterpret_cast<uint4*>(img + DRec::gh + at) = hi;
-                *reinterpret_cast<uint4*>(img + DRec::gm + at) = lo;
-            }
-        }
-    }
+    if (tid == 0) *reinterpret_cast<uint32_t*>(img2 + DRec::there) = kThere;
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -455,8 +417,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         if (s_abort) {
             // nothing in flight when TMEM and shared memory are given back
             mbar_wait_bounded(bar_in, 0, a.wait_ns);
-            if (elect_one()) tc_commit(bar_mma);
-            for (int i = 0; i < 2; ++i) mbar_wait_bounded(bar_mma, i, a.wait_ns);
+            if (elect_one()) tc_commit(bar_drain);
+            mbar_wait_bounded(bar_drain, 0, a.wait_ns);
         }
         tmem_free(tm, DPrep::cols);
         uint8_t* record = ca.records + ((size_t)blk * a.H + h) * DRec::bytes;
@@ -466,7 +428,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                 atomicOr(a.status, DAMP_EFLAG_TIMEOUT);
             }
         } else if (elect_one()) {
-            bulk_s2g(record, smem_u32(sm + DPrep::img), DRec::bytes);
+            bulk_s2g(record, smem_u32(img), DRec::ph);
+            bulk_s2g(record + DRec::ph, smem_u32(img2 + DRec::ph), DRec::bytes - DRec::ph);
             bulk_commit();
             bulk_wait_read<0>();
         }
@@ -476,15 +439,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // ------------------------------------------------------------------ delta: chain
 
 // One CTA of 22 warps a (request, head): 16 keep the state and form the A
-// operands (warp w: TMEM lanes of w & 3, a quarter of the columns), 4 write the
-// readout, one loads, one issues the matrix instructions.
+// operands (warp w: TMEM lanes of w & 3, a quarter of the columns), 4 form U's
+// pair and write the readout, one loads, one issues the matrix instructions.
 //
-// What bounds it is the chain of one block after another: S as a pair -> K S ->
-// R as a pair -> U -> U as a pair -> the block's part of S -> S.  So Q S and
-// G R are products of their own behind the ones the chain waits for (K and Q
-// as one operand of 128 rows cost 1280 cycles against 768 + 768, but the chain
-// waits for all of them), and S's update and K S go by halves of the key
-// channels: one half's product runs while the other half's state is split.
+// What bounds it is the chain of one block after another: S as three terms -> K S
+// -> R as terms -> U -> U as terms -> the block's part of S -> S.  So Q S and P U
+// are products of their own behind the ones the chain waits for (K and Q as one
+// operand of 128 rows cost less, but the chain waits for all of them), and S's
+// update and K S go by halves of the key channels: one half's product runs while
+// the other half's state is split.
 struct DChain {
     static constexpr int kWarps = 16, kOut = 4;              // state warps, readout warps
     static constexpr int kStages = 2;
@@ -503,11 +466,12 @@ struct DChain {
                                             // second half: the first half's next terms are written while the
                                             // second half's product still reads U
     static constexpr uint32_t KS = 320;     // (K S)^T, FP32 [128][64], then U^T in its place: R is formed, and
-                                            // K S with it read, before T' R is issued
-    static constexpr uint32_t QS = 384, GR = 448;   // (Q S)^T, (G R)^T
-    // Barriers.  B*: a product is done (KS; U; Q S and G R; S's two halves).  C*: the state
-    // warps have left an operand in TMEM (S's halves, R, U); CO: the readout is out of TMEM.
-    enum { Full = 0, Empty = kStages, BK = 2 * kStages, BU, BO, BS, CS = BS + 2, CR = CS + 2, CU, CO, Drain };
+                                            // K S with it read, before T' R is issued.  Then U^T hi and mid for
+                                            // P U: 16 tokens' 8 + 8 columns over the 16 they were read from
+    static constexpr uint32_t QS = 384, PU = 448;   // (Q S)^T, (P U)^T
+    // Barriers.  B*: a product is done (KS; U; Q S and P U; S's two halves).  C*: the state warps have
+    // left an operand in TMEM (S's halves, R, diag(w) U), the readout's U; CO: the readout is out of TMEM.
+    enum { Full = 0, Empty = kStages, BK = 2 * kStages, BU, BO, BS, CS = BS + 2, CR = CS + 2, CU, CV, CO, Drain };
 };
 
 __global__ void __launch_bounds__(DChain::threads, 1)
@@ -576,6 +540,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             mbar_init(bar(X::CS + 1), X::kWarps / 2);
             mbar_init(bar(X::CR), X::kWarps);
             mbar_init(bar(X::CU), X::kWarps);
+            mbar_init(bar(X::CV), X::kOut);
             mbar_init(bar(X::CO), X::kOut);
             mbar_init(bar(X::Drain), 1);
             fence_mbar_init();
@@ -738,8 +703,8 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = __fmaf_rn(gc, S[i], __uint_as_float(y[i]));
-            // The stage is used up: the second half's product was its last reader, and
-            // every state warp had its values out before that product was issued.
+            // Of the state's side the stage is used up: every state warp had its values out before the
+            // second half's product was issued.  (P U is the readout's.)
             if (part >= 2 && lane == 0) mbar_arrive(bar(X::Empty + c % X::kStages));
         }
         // (all state warps are here, or none: the waits that leave the loop are waits of all)
@@ -756,6 +721,22 @@ __global__ void __launch_bounds__(DChain::threads, 1)
         uint8_t* so = sm + X::out;
         for (int c = 0; c < nc; ++c) {
             const float* gam = reinterpret_cast<const float*>(sm + (c % X::kStages) * X::stage + X::rec + DRec::gam);
+            // U as a pair for P U, once the state warps have read it (8192 tokens x 32 heads: 50 us more where
+            // they form it themselves)
+            if (!wait_group(warp == X::kWarps, X::CU, c & 1, 1, X::kOut * 32)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {
+                uint32_t x[16], u[16];
+                tmem_ld16(lanes + X::KS + part * 16, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    split_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), u[i], u[8 + i]);
+                tmem_st16(lanes + X::KS + part * 16, u);
+            }
+            tmem_wait_st();
+            arrive(X::CV);
             if (!wait_group(warp == X::kWarps, X::BO, c & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             // out of TMEM first: the next block's Q S waits for that
@@ -763,7 +744,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             for (int part = 0; part < 4; ++part) {
                 uint32_t o1[16], o2[16];
                 tmem_ld16(lanes + X::QS + part * 16, o1);
-                tmem_ld16(lanes + X::GR + part * 16, o2);
+                tmem_ld16(lanes + X::PU + part * 16, o2);
                 float2 gt[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) gt[i] = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
@@ -813,7 +794,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             const uint32_t st = base + (c % X::kStages) * X::stage, rec = st + X::rec;
             const uint32_t ph = c & 1;
             if (!wait_all(X::Full + c % X::kStages, (c / X::kStages) & 1)) break;
-            if (c > 0 && !wait_all(X::CO, ph ^ 1)) break;
+            if (c > 0 && !wait_all(X::BO, ph ^ 1)) break;     // (P U read the columns that K S is written to)
             // (K S)^T, the channels' first half as soon as it is there.  Small terms go first here and
             // below: the tensor core truncates its sums, the less the smaller they are.
             bool ok = true;
@@ -826,19 +807,20 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                     for (int ks = 0; ks < 12; ++ks)
                         mma_ts(tm + X::KS, tm + X::S + (2 - (ks >> 2)) * 64 + half * 32 + (ks & 3) * 8,
                                desc_k_major(st + X::kq + half * kTile + (ks & 3) * 32), idk, half + ks > 0);
-                    if (half == 1) {
-                        tc_commit(bar(X::BK));
-                        // (Q S)^T, hi and mid, while the state warps work on R
-#pragma unroll
-                        for (int ks = 0; ks < 16; ++ks)
-                            mma_ts(tm + X::QS, tm + X::S + 8 * ks,
-                                   desc_k_major(st + X::kq + ((ks >> 2) & 1) * kTile + kHalf + (ks & 3) * 32),
-                                   idk, ks > 0);
-                    }
+                    if (half == 1) tc_commit(bar(X::BK));
                 }
             }
             if (!ok) break;
-            // U^T = (T' R)^T in six products of terms, then (G R)^T: hi * hi, mid * hi, hi * mid
+            // (Q S)^T, hi and mid, while the state warps work on R
+            if (c > 0 && !wait_all(X::CO, ph ^ 1)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 16; ++ks)
+                    mma_ts(tm + X::QS, tm + X::S + 8 * ks,
+                           desc_k_major(st + X::kq + ((ks >> 2) & 1) * kTile + kHalf + (ks & 3) * 32), idk, ks > 0);
+            }
+            // U^T = (T' R)^T in six products of terms
             if (!wait_all(X::CR, ph)) break;
             tc_fence_after();
             if (elect_one()) {
@@ -848,11 +830,6 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                     mma_ts(tm + X::KS, tm + X::R + r[ks >> 2] * 32 + 8 * (ks & 3),
                            desc_k_major(rec + t[ks >> 2] * kMat + (ks & 3) * 32), idk, ks > 0);
                 tc_commit(bar(X::BU));
-#pragma unroll
-                for (int ks = 0; ks < 12; ++ks)
-                    mma_ts(tm + X::GR, tm + X::R + 8 * (ks & 7),
-                           desc_k_major(rec + (ks < 8 ? DRec::gh : DRec::gm) + (ks & 3) * 32), idk, ks > 0);
-                tc_commit(bar(X::BO));
             }
             // the block's part of S^T, by halves of its channels
             if (!wait_all(X::CU, ph)) break;
@@ -866,6 +843,16 @@ __global__ void __launch_bounds__(DChain::threads, 1)
                                desc_mn_major(st + X::kq + half * kTile + (ks & 3) * 2048, kTile), idmn, ks > 0);
                     tc_commit(bar(X::BS + half));
                 }
+            }
+            // (P U)^T: mid * hi, hi * mid, hi * hi, while the state warps work on S
+            if (!wait_all(X::CV, ph)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 12; ++ks)
+                    mma_ts(tm + X::PU, tm + X::KS + (ks & 3) * 16 + (ks < 4 ? 8 : 0),
+                           desc_k_major(rec + (ks >> 2 == 1 ? DRec::pm : DRec::ph) + (ks & 3) * 32), idk, ks > 0);
+                tc_commit(bar(X::BO));
             }
         }
         // nothing in flight when TMEM and shared memory are given back

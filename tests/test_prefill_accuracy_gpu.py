@@ -19,9 +19,9 @@ def i32(x):
 # 16 half steps of the largest it was.  Half steps of the kernels between two states: operands of products
 # T' 3 (A's two factors, the inverse), R 2, diag(w) U 2; sums of up to 24 matrix instructions, truncated (2
 # each) and independent: 2 sqrt(24) = 9.8; in all 16, where the FP32 form has one at least.
-# A readout is rounded to bf16, and the operands of its products (S, R, P, T', G) are pairs of bf16 values,
-# which leave 2^-17 of them; with the dropped products of two second terms at most 8 such parts.
-STEPS, SPLITS = 16, 8 * 2.0 ** -17
+# A readout is rounded to bf16, and the operands of its products (S in Q S, P and U in P U) are pairs of bf16
+# values, which leave 2^-17 of them; with the dropped product of two second terms at most 4 such parts.
+STEPS, SPLITS = 16, 4 * 2.0 ** -17
 
 
 def blocks(rule, q, k, v, alpha, beta, S0, dtype):
@@ -38,15 +38,13 @@ def blocks(rule, q, k, v, alpha, beta, S0, dtype):
             Gam[:, t, t] = 1.0
         gam, w = torch.cumprod(a, 1), Gam[:, -1, :, None]
         P = Gam * (Q @ K.transpose(1, 2))
-        U, R, T = V, V, None
+        U = V
         if rule == "delta":
             A = torch.tril(be[..., None] * Gam * (K @ K.transpose(1, 2)), -1)
             I = torch.eye(n, dtype=dtype).expand_as(A)
             T = torch.linalg.solve_triangular(I + A, I, upper=False) * be[:, None]
-            R = V - gam[..., None] * (K @ S)
-            U = T @ R
-        sums.append(gam[..., None] * (Q.abs() @ S.abs()) +
-                    P.abs() @ (R.abs() if T is None else T.abs() @ R.abs()))
+            U = T @ (V - gam[..., None] * (K @ S))
+        sums.append(gam[..., None] * (Q.abs() @ S.abs()) + P.abs() @ U.abs())
         S = gam[:, -1, None, None] * S + K.transpose(1, 2) @ (w * U)
     return S, torch.cat(sums, 1).transpose(0, 1)
 
