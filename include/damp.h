@@ -324,12 +324,13 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
  * plan's, H <= 65535, and n * H and blocks * H below 2^31.
  * Arithmetic: FP32, token by token, and the readout rounded once; bf16 layers
  * with d_k = d_v = 128 run in blocks of 64 tokens on the tensor cores.  There a
- * delta-rule state is as good as FP32 sums of the block form: about 1e-6 of its
- * norm for keys in many directions, up to 3e-5 where the keys of a block are all
- * equal and beta |k|^2 nears 2 (beyond 2 the recurrence itself grows without
- * bound).  diag(w) V of the decay rule and the operands of a readout's products
- * enter as two bf16 values, which lose up to 2^-17 of them; a readout is rounded
- * to bf16 behind that.  The same call gives the same bits.
+ * state is as good as FP32 sums of the block form: a few 1e-6 of its norm or less
+ * for the decay rule and for the delta rule with keys in many directions, up to
+ * 4e-5 where the keys of a block are all equal up to their sign and beta |k|^2
+ * nears 2 (beyond 2 the recurrence itself grows without bound).  The FP32
+ * operands of products that only a readout is made of enter as two bf16 values,
+ * which lose up to 2^-17 of them; the readout is rounded to bf16 behind that.
+ * The same call gives the same bits.
  * A wait inside the call that runs out sets DAMP_EFLAG_TIMEOUT; the results of
  * that call are not valid.  A (request, head) whose work it kept from being done
  * keeps its state (quantized pools: as packed again from what the call unpacked,

@@ -24,16 +24,17 @@
 // sums drift).
 //
 // Precision: Q, K and V enter as the bf16 they are, accumulation is FP32.  The
-// delta rule's FP32 operands of whatever a state is made of (S in K S, T' and R
-// in T' R, diag(w) U) enter as three bf16 terms, which hold all their bits; the
-// product of two such keeps every pair of terms down to 2^-18 (6 of 9).  Pairs
-// are not enough there: with equal keys T' alternates in sign, T' R cancels, and
-// what the pairs had lost came to 1e-3 of the state (beta |k|^2 = 1.9, where the
-// recurrence is stable and FP32 sums of the same form keep 2e-5).
-// What only a readout is made of (P and U in P U, S in Q S), and the decay rule's
-// diag(w) V, enters as a pair, hi + mid, which leaves 2^-17 of it: a readout is
-// rounded to bf16 (2^-8) afterwards.  (As G R with G = P T', which needs no U, the
-// readout would cancel as T' R does: 1.4e-3 of it lost with equal keys.)
+// FP32 operands of whatever a state is made of (S in K S, T' and R in T' R,
+// diag(w) U; diag(w) V of the decay rule) enter as three bf16 terms, which hold
+// all their bits; the product of two such keeps every pair of terms down to
+// 2^-18 (6 of 9).  Pairs are not enough there: with equal keys T' alternates in
+// sign, T' R cancels, and what the pairs had lost came to 1e-3 of the state
+// (beta |k|^2 = 1.9, where the recurrence is stable and FP32 sums of the same
+// form keep 2e-5); values that cancel under a slow decay lost 3e-4.
+// What only a readout is made of (P and U in P U, P V, S in Q S) enters as a
+// pair, hi + mid, which leaves 2^-17 of it: a readout is rounded to bf16 (2^-8)
+// afterwards.  (As G R with G = P T', which needs no U, the readout would cancel
+// as T' R does: 1.4e-3 of it lost with equal keys.)
 //
 // Decays are running products, never quotients or exponentials of sums: a
 // decay of zero inside a block, or products that underflow, need no care.
@@ -875,7 +876,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
 // multiplies the decays up), one issues the matrix instructions.  Without the
 // delta rule a block's part of S does not depend on S, so operands are formed
 // ahead and the tensor core always has a product to work on (cycles a block):
-//   dS = (diag(w) V)^T K   A pair in TMEM                                    640
+//   dS = (diag(w) V)^T K   A hi and mid in TMEM, lo in shared memory (TMEM is full)   1088
 //   S^T Q^T                A pair in TMEM                                    768
 //   Q K^T                  of the next block, as two products of 32 columns
 //                          whose tokens lie in lanes 0..63 and 64..127: all
@@ -891,14 +892,15 @@ struct EChain {
     static constexpr int threads = 32 * (wMma + 1);
     static constexpr int kStages = 3;
     static constexpr int k = 0, v = kTile, q = 2 * kTile, stage = 3 * kTile;
-    static constexpr int p = kStages * stage;                 // P pair [2][hi, lo]
-    static constexpr int out = p + 2 * 2 * kMat;
+    static constexpr int p = kStages * stage;                 // P pair [2][hi, mid]
+    static constexpr int lo = p + 2 * 2 * kMat;               // (diag(w) V)^T lo of two blocks, K-major [128 v][64 t]
+    static constexpr int out = lo + 2 * kTile;                // half a block's readout rows, 16 bytes apart in banks
     static constexpr int out_row = D * 2 + 16;
-    static constexpr int ring = out + C * out_row;            // alpha, gamma, w, mid of four blocks
+    static constexpr int ring = out + C / 2 * out_row;        // alpha, gamma, w, mid of four blocks
     static constexpr int bar = ring + 4 * 4 * C * 4;
     static constexpr int bytes = bar + 256 + 1024;
     // TMEM columns.  dS's first 64 hold the next block's Q K^T between two uses.
-    static constexpr uint32_t dS = 0, Sh = 128, O1 = 256, O2 = 320, V = 384;   // V: pairs of two blocks, 64 each
+    static constexpr uint32_t dS = 0, Sh = 128, O1 = 256, O2 = 320, V = 384;   // V: hi, mid of two blocks, 64 each
     // Barriers.  Full: a block's tiles and decays are there.  BD, BQ, BP: dS, S^T Q^T, Q K^T done; BO:
     // V^T P^T too.  CV, CP: diag(w) V, P are there; CD, CP0: dS, Q K^T are out of TMEM; CS: S's pair is
     // there; CO: the readout is out of TMEM.  Where a waiter can be a block behind there are two.
@@ -1094,7 +1096,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
         constexpr int kN = X::kForm * 32;
         const int group = (warp - X::kWarps) / X::kForm, kId = 2 + group, lead = X::kWarps + group * X::kForm;
         const int ft = tid - lead * 32, c2 = (lane & 3) * 2;
-        // diag(w) V of block c as a pair in TMEM
+        // diag(w) V of block c as three terms, hi and mid in TMEM
         auto form_v = [&](int c) -> bool {
             const uint32_t st = base + c % X::kStages * X::stage, buf = c & 1;
             const int live = min(C, len - c * C);
@@ -1109,14 +1111,15 @@ __global__ void __launch_bounds__(EChain::threads, 1)
                     *reinterpret_cast<uint4*>(stp + X::v + to) = make_uint4(0, 0, 0, 0);
                 }
             }
-            // the block before last has used this pair up
+            // the block before last has used these terms up
             if (!wait_group(c >= 2 && warp == lead, X::BD + buf, ((c >> 1) - 1) & 1, kId, kN)) return false;
             tc_fence_after();
             const float* w = ring(c) + 2 * C;
 #pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {   // 16 value columns (TMEM lanes) each, transposed by ldmatrix
-                uint32_t hi[16], lo[16];
+                uint32_t hi[16], mid[16];
                 const int col = quad * 32 + hf * 16;
+                uint8_t* lop = sm + X::lo + buf * kTile;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // 16 tokens each
                     uint32_t v[4];
@@ -1128,12 +1131,15 @@ __global__ void __launch_bounds__(EChain::threads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 x = make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
-                        split_bf16(__fmul2_rn(x, i < 2 ? w0 : w1), hi[4 * j + i], lo[4 * j + i]);
+                        uint32_t lo;               // of column l / 4 + 8 (i & 1), tokens 16 j + 8 (i / 2) + 2 (l % 4), + 1
+                        split3_bf16(__fmul2_rn(x, i < 2 ? w0 : w1), hi[4 * j + i], mid[4 * j + i], lo);
+                        *reinterpret_cast<uint32_t*>(lop + swz(col + (lane >> 2) + 8 * (i & 1),
+                                                               j * 32 + (i >> 1) * 16 + c2 * 2)) = lo;
                     }
                 }
                 const uint32_t to = lanes + ((uint32_t)(hf * 16) << 16) + X::V + buf * 64;
                 tmem_st_16x128(to, hi);
-                tmem_st_16x128(to + 32, lo);
+                tmem_st_16x128(to + 32, mid);
             }
             fence_proxy_async_smem();
             tmem_wait_st();
@@ -1193,43 +1199,48 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             const float* gam = ring(c) + C;
             if (!wait_group(warp == X::wOut, X::BO + (c & 1), (c >> 1) & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
+            const int live = min(C, len - c * C);
             // (Not unrolled, as other long loops of this kernel are not: two SMs share an instruction
             // cache that the unrolled roles together do not fit.  16 ragged requests of 8192 tokens,
             // 32 heads: 131 us unrolled, 125 so.  The delta chain's roles wait for one another most of
             // the time, and only its readout is better off: with its other loops not unrolled either,
             // 8192 tokens x 32 heads took 460 us against 430.)
 #pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-                uint32_t o1[16], o2[16];
-                tmem_ld16(lanes + X::O1 + part * 16, o1);
-                tmem_ld16(lanes + X::O2 + part * 16, o2);
-                float2 gt[8];
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+                for (int part = 2 * half; part < 2 * half + 2; ++part) {
+                    uint32_t o1[16], o2[16];
+                    tmem_ld16(lanes + X::O1 + part * 16, o1);
+                    tmem_ld16(lanes + X::O2 + part * 16, o2);
+                    float2 gt[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) gt[i] = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
-                tmem_wait_ld();
-                // (the loader may write over these decays once the block after next is loaded, which
-                // this arrival lets happen: they are read before it)
-                if (part == 3) arrive(X::CO);
+                    for (int i = 0; i < 8; ++i) gt[i] = *reinterpret_cast<const float2*>(gam + part * 16 + 2 * i);
+                    tmem_wait_ld();
+                    // (the loader may write over these decays once the block after next is loaded, which
+                    // this arrival lets happen: they are read before it)
+                    if (part == 3) arrive(X::CO);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t o = pack_bf16(
-                        __fmaf_rn(gt[i].x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
-                        __fmaf_rn(gt[i].y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
-                    uint8_t* to = so + (part * 16 + 2 * i) * X::out_row + vcol * 2;
-                    *reinterpret_cast<uint16_t*>(to) = (uint16_t)o;
-                    *reinterpret_cast<uint16_t*>(to + X::out_row) = (uint16_t)(o >> 16);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t o = pack_bf16(
+                            __fmaf_rn(gt[i].x, __uint_as_float(o1[2 * i]), __uint_as_float(o2[2 * i])),
+                            __fmaf_rn(gt[i].y, __uint_as_float(o1[2 * i + 1]), __uint_as_float(o2[2 * i + 1])));
+                        uint8_t* to = so + ((part & 1) * 16 + 2 * i) * X::out_row + vcol * 2;
+                        *reinterpret_cast<uint16_t*>(to) = (uint16_t)o;
+                        *reinterpret_cast<uint16_t*>(to + X::out_row) = (uint16_t)(o >> 16);
+                    }
                 }
-            }
-            bar_sync(1, X::kOut * 32);
-            const int live = min(C, len - c * C);
+                // (rows of 256 bytes from shared memory: a warp's own 64 bytes of each, as they come, took 156 us
+                // for the 16 requests)
+                bar_sync(1, X::kOut * 32);
 #pragma unroll
-            for (int i = 0; i < C * 16 / (X::kOut * 32); ++i) {
-                const int r = (wt >> 4) + i * (X::kOut * 2), u = wt & 15;
-                if (r < live)
-                    *reinterpret_cast<uint4*>(out + (size_t)(c * C + r) * a.H * D + u * 8) =
-                        *reinterpret_cast<const uint4*>(so + r * X::out_row + u * 16);
+                for (int i = 0; i < C / 2 * 16 / (X::kOut * 32); ++i) {
+                    const int r = (wt >> 4) + i * (X::kOut * 2), u = wt & 15, t = half * (C / 2) + r;
+                    if (t < live)
+                        *reinterpret_cast<uint4*>(out + (size_t)(c * C + t) * a.H * D + u * 8) =
+                            *reinterpret_cast<const uint4*>(so + r * X::out_row + u * 16);
+                }
+                bar_sync(1, X::kOut * 32);
             }
-            bar_sync(1, X::kOut * 32);
         }
     } else if (warp == X::wLoad) {
         // ---------------------------------------------------------- loads
@@ -1306,9 +1317,13 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll 4
-                for (int ks = 0; ks < 8; ++ks)
+                for (int ks = 0; ks < 4; ++ks)       // lo, then mid and hi
+                    mma_ss(tm + X::dS, desc_k_major(base + X::lo + ph * kTile + ks * 32),
+                           desc_mn_major(st + X::k + ks * 2048, kHalf), ids, ks > 0);
+#pragma unroll 4
+                for (int ks = 7; ks >= 0; --ks)
                     mma_ts(tm + X::dS, tm + X::V + ph * 64 + 8 * ks,
-                           desc_mn_major(st + X::k + (ks & 3) * 2048, kHalf), ids, ks > 0);
+                           desc_mn_major(st + X::k + (ks & 3) * 2048, kHalf), ids, 1);
                 tc_commit(bar(X::BD + ph));
                 if (SUM) tc_commit(bar(X::Empty + c % X::kStages));
             }

@@ -85,7 +85,7 @@ KEYS = ["decayed", "random", "equal:1", "equal:1.9", "alternating:1.9", "four:1.
 
 @pytest.mark.parametrize("past", [0, 1])
 @pytest.mark.parametrize("rule,name", [("delta", n) for n in KEYS] +
-                         [("decay", n) for n in ("decayed", "random", "long", "short")])
+                         [("decay", n) for n in ("decayed", "random", "long", "short", "cancel")])
 def test_states_are_as_good_as_fp32_sums(rule, name, past):
     H, lengths = 3, [512, 100, 64]
     g = torch.Generator().manual_seed(sum(map(ord, name)) + past)
