@@ -368,11 +368,15 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
  *                   core form is two kernels (delta rule; decay rule in
  *                   segments), the first one alone leaves its first loads
  *                   unissued.
+ *                   DAMP_HOOK_NO_TENSOR_MAPS: the driver's tensor-map encoder
+ *                   counts as not there; only damp_prefill of bf16 layers with
+ *                   d_k = d_v = 128 needs it, and fails with DAMP_ERR_CUDA.
  * Process-wide, for the launches enqueued after the call.
  */
 #define DAMP_HOOK_HOLD_FIRST_ITEM 1u
 #define DAMP_HOOK_FAIL_HALF 2u
 #define DAMP_HOOK_HOLD_FIRST_KERNEL 4u
+#define DAMP_HOOK_NO_TENSOR_MAPS 8u
 int damp_set_test_hooks(uint64_t wait_limit_ns, uint32_t hooks);
 
 /*

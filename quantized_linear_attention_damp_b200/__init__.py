@@ -34,6 +34,7 @@ DAMP_EFLAG_NONFINITE = 4
 DAMP_HOOK_HOLD_FIRST_ITEM = 1
 DAMP_HOOK_FAIL_HALF = 2
 DAMP_HOOK_HOLD_FIRST_KERNEL = 4
+DAMP_HOOK_NO_TENSOR_MAPS = 8
 
 DAMP_FMT_FP32 = 0
 DAMP_FMT_INT8_ROW = 1

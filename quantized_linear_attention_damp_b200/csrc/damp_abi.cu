@@ -62,6 +62,10 @@ size_t header_bytes(int H, int d_k) {
     return align_up(damp::head_table_offset(H, d_k) + (size_t)H * 16, 256);
 }
 
+// Test hooks of the failure path (damp_set_test_hooks).
+std::atomic<unsigned long long> g_wait_ns{0};
+std::atomic<uint32_t> g_hooks{0};
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? DAMP_OK : DAMP_ERR_CUDA; }
 
 bool is_fp16_row(const PoolDesc& d, int h, int i) {
@@ -228,7 +232,11 @@ int create_common(int format, int n_slots, int H, int d_k, int d_v, int hp_rows,
         }
         cudaError_t e = cudaMemcpy(dev_buf, hdr.data(), hdr.size(), cudaMemcpyHostToDevice);
         if (e == cudaSuccess) e = damp::prepare_decode(d);
-        if (e == cudaSuccess && d.d_k == 128 && d.d_v == 128) e = damp::prepare_prefill();
+        // (What the block prefill needs may be missing: no other call of the pool needs it, and the
+        // prefill's launch asks again and says so.)
+        if (e == cudaSuccess && d.d_k == 128 && d.d_v == 128 &&
+            damp::prepare_prefill(g_hooks.load(std::memory_order_relaxed)) != cudaSuccess)
+            (void)cudaGetLastError();
         if (e != cudaSuccess) {
             delete[] p->d.host_masks;
             delete[] p->d.host_heads;
@@ -379,10 +387,6 @@ int damp_pool_unpack(const damp_pool* pool, int n, const int32_t* slot_idx, floa
 }  // extern "C"
 
 namespace {
-
-// Test hooks of the failure path (damp_set_test_hooks).
-std::atomic<unsigned long long> g_wait_ns{0};
-std::atomic<uint32_t> g_hooks{0};
 
 int decode_common(const damp_pool* pool, int n, const int32_t* slot_idx, int in_dtype,
                   const void* q, const void* k, const void* v, int gate, const float* alpha,
@@ -656,7 +660,8 @@ int damp_prefill(const damp_pool* pool, int rule, int n, int max_tokens,
 }
 
 int damp_set_test_hooks(uint64_t wait_limit_ns, uint32_t hooks) {
-    if (hooks & ~(DAMP_HOOK_HOLD_FIRST_ITEM | DAMP_HOOK_FAIL_HALF | DAMP_HOOK_HOLD_FIRST_KERNEL))
+    if (hooks & ~(DAMP_HOOK_HOLD_FIRST_ITEM | DAMP_HOOK_FAIL_HALF | DAMP_HOOK_HOLD_FIRST_KERNEL |
+                  DAMP_HOOK_NO_TENSOR_MAPS))
         return DAMP_ERR_INVALID_ARGUMENT;
     g_wait_ns.store(wait_limit_ns, std::memory_order_relaxed);
     g_hooks.store(hooks, std::memory_order_relaxed);

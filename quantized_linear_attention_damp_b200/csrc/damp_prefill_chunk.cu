@@ -1408,7 +1408,8 @@ size_t first_block_bytes(int n) { return ((size_t)n * 4 + 255) / 256 * 256; }
 
 // The driver's encoder and the kernels' attributes, once per device (the
 // current one).
-cudaError_t prepare_prefill() {
+cudaError_t prepare_prefill(uint32_t hooks) {
+    if (hooks & kHookNoTensorMaps) return cudaErrorNotSupported;
     static std::atomic<uint64_t> ready{0};             // a bit per device below 64
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1440,7 +1441,7 @@ size_t prefill_chunk_bytes(int n, int H, int max_tokens, int max_blocks, int del
 
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
-    cudaError_t e = prepare_prefill();
+    cudaError_t e = prepare_prefill(a.hooks);
     if (e == cudaSuccess) e = token_map(&mq, a.q, a.H_qk, a.max_tokens, a.q_stride);
     if (e == cudaSuccess) e = token_map(&mk, a.k, a.H_qk, a.max_tokens, a.k_stride);
     if (e == cudaSuccess) e = token_map(&mv, a.v, a.H, a.max_tokens, a.v_stride);

@@ -5,9 +5,11 @@
 
 namespace damp {
 
-// Test hooks of the prefill's block kernels (DAMP_HOOK_FAIL_HALF, DAMP_HOOK_HOLD_FIRST_KERNEL).
+// Test hooks of the prefill's block kernels (DAMP_HOOK_FAIL_HALF, DAMP_HOOK_HOLD_FIRST_KERNEL,
+// DAMP_HOOK_NO_TENSOR_MAPS).
 constexpr uint32_t kHookFailHalf = 2u;
 constexpr uint32_t kHookHoldFirstKernel = 4u;
+constexpr uint32_t kHookNoTensorMaps = 8u;
 
 // Arguments of the batch-plan kernel (damp_plan.cu).
 struct PlanArgs {
@@ -62,9 +64,10 @@ cudaError_t launch_decay_step(const StepArgs& a, int in_dtype, int H_qk, cudaStr
 // Prompts, token by token (damp_prefill.cu): every shape and input type.
 cudaError_t launch_prefill_tokens(const PrefillArgs& a, cudaStream_t stream);
 // Prompts in blocks of 64 tokens on the tensor cores (damp_prefill_chunk.cu):
-// bf16 inputs, 128 x 128 states.  prepare_prefill sets the kernels' attributes
-// (damp_pool_create calls it, outside any stream capture).
-cudaError_t prepare_prefill();
+// bf16 inputs, 128 x 128 states.  prepare_prefill looks up the driver's tensor-
+// map encoder and sets the kernels' attributes (damp_pool_create calls it ahead of
+// the first prefill, whose launch asks again and reports what is missing).
+cudaError_t prepare_prefill(uint32_t hooks);
 bool prefill_chunk_fits(int d_k, int d_v, int bf16);
 size_t prefill_chunk_bytes(int n, int H, int max_tokens, int max_blocks, int delta);
 cudaError_t launch_prefill_chunk(const PrefillArgs& a, cudaStream_t stream);

@@ -92,3 +92,27 @@ def test_the_first_of_two_kernels_runs_out(rule, lengths, fmt):
     kept = ((values[0] - values[1]).abs() <= 0.51 * step).flatten(1).all(dim=1)
     assert torch.isfinite(values[1]).all()
     assert kept.sum() >= n + 1 - (300 in lengths), kept
+
+
+def test_a_pool_without_tensor_maps():
+    """Where the driver's tensor-map encoder cannot be had, only the calls that need it fail."""
+    n, H, d, T = 2, 2, 128, 20
+    x = inputs(torch.Generator().manual_seed(1), T, H, H, d, d, BF)
+    plan = D.BatchPlan(n, T, n).build(i32([15, 5]), i32([1, 0]))
+    try:
+        D.damp_set_test_hooks(hooks=D.DAMP_HOOK_NO_TENSOR_MAPS)
+        pool = D.DampPool("mixed", n, H, d, np.stack([np.arange(27)] * H))
+        pool.pack(i32([0, 1]), torch.zeros(n, H, d, d, device="cuda"))
+        one = {c: x[c][:n].contiguous() for c in x}
+        out = torch.empty(n, H, d, device="cuda")
+        pool.step(i32([0, 1]), one["q"], one["k"], one["v"], one["alpha"], one["beta"], out)
+        wide = pool.prefill(plan, *(x[c].float() for c in ("q", "k", "v", "alpha", "beta")))
+        assert out.any() and wide.any()
+        args = (plan, x["q"], x["k"], x["v"], x["alpha"], x["beta"])
+        with pytest.raises(D.DampError) as e:
+            pool.prefill(*args)
+        assert e.value.status == D.DAMP_ERR_CUDA
+    finally:
+        D.damp_set_test_hooks()
+    assert pool.prefill(*args).any() and pool.get_error() == 0
+    pool.close()
