@@ -1,0 +1,65 @@
+"""The forms of the decay-rule step and of the token prefill that only larger batches take.  Each case computes
+the rule that chooses its form, so that a change of the rule shows here."""
+import numpy as np
+import pytest
+import torch
+
+from tests import test_decay_step_gpu as step
+from tests import test_prefill_gpu as prefill
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ["fp32", "int8", "mixed", "fp8"]
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def warp_per_unit(units, dv):
+    return 3 * units >= 2 * 8 * sms() * (3 if dv <= 128 else 2)
+
+
+def with_padding(n):
+    slot = np.random.default_rng(n).permutation(n + 2)[:n].astype(np.int32)
+    slot[::7] = -1
+    return slot
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dk,dv,n,H,Hqk", [(32, 48, 250, 10, 5), (48, 128, 250, 10, 10), (16, 208, 170, 10, 2),
+                                           (16, 256, 164, 10, 1)])
+def test_step_with_a_warp_per_state(fmt, dk, dv, n, H, Hqk):
+    """All lanes of a warp in use and not, one and two column groups a lane, padding between live entries;
+    more states than warps, so that a warp goes on to a next state."""
+    assert warp_per_unit(n * H, dv)
+    assert step.run(fmt, dk, dv, n, H, Hqk, "bf16", slot_idx=with_padding(n)) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_step_with_a_warp_per_state_and_several_states_a_warp(fmt):
+    n, H, dk, dv = 520, 16, 16, 112
+    assert n * H > 2 * 3 * 8 * sms()
+    assert step.run(fmt, dk, dv, n, H, 8, "f32", steps=1, slot_idx=with_padding(n)) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dk,dv,n,H,Hqk", [(96, 160, 60, 10, 5), (112, 128, 100, 10, 2), (128, 128, 60, 10, 10)])
+def test_step_with_a_cta_per_state_and_several_states_a_cta(fmt, dk, dv, n, H, Hqk):
+    assert not warp_per_unit(n * H, dv) and n * H > sms() * (3 if dv <= 128 else 2)
+    assert step.run(fmt, dk, dv, n, H, Hqk, "bf16", steps=1, slot_idx=with_padding(n)) == 0
+
+
+@pytest.mark.parametrize("rule", ["decay", "delta"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dk,dv", [(16, 144), (32, 16), (48, 80), (64, 64), (96, 48), (128, 112), (208, 16), (256, 48)])
+def test_prompts_with_32_rows_a_lane(rule, dtype, dk, dv):
+    """Many requests and heads: a lane holds 32 key rows (1, 2, 4 or 8 lanes a column), with padding rows behind
+    d_k and column groups that d_v does not fill."""
+    n, H = 40, 12
+    lanes = 1 if dk <= 32 else 2 if dk <= 64 else 4 if dk <= 128 else 8
+    assert n * H * -(-dv * lanes // 128) >= 3 * sms()
+    g = np.random.default_rng(dk + dv)
+    lengths = g.integers(0, 12, n).tolist()
+    lengths[5], lengths[9] = 33, 64
+    prefill.check(rule, lengths, H=H, Hqk=4, dk=dk, dv=dv, dtype=dtype, past=g.integers(0, 2, n).tolist(), spare=3)
