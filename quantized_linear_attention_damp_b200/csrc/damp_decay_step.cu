@@ -110,9 +110,9 @@ __global__ void __launch_bounds__(kDecayThreads) decay_step_kernel(const StepArg
 // stored: first the byte rows, then the FP16 rows, in batches of 8 rows of one
 // format (4 of FP32 states) and no test per row; q and k are put into that order
 // once per unit.  A batch is one run of bytes: the warp copies it into its own
-// ring in shared memory by asynchronous 16-byte copies, three batches ahead and
-// across units (one batch ahead in registers kept 16 KB an SM in flight and
-// reached 3 TB/s).  Lane l holds the column groups (of 4) l and, for d_v > 128
+// ring in shared memory by asynchronous 16-byte copies, two batches ahead (one for
+// d_v > 128) and across units (one batch ahead in registers kept 16 KB an SM in
+// flight and reached 3 TB/s).  Lane l holds the column groups (of 4) l and, for d_v > 128
 // (G = 2), l + 32.  One lane per row computes the row's scale: one division for
 // 8 rows, not 8 by every lane.
 //   SOLO: a warp owns a unit and all its batches; no barrier, no sum over
