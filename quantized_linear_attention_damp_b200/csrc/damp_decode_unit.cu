@@ -397,16 +397,17 @@ __global__ void __launch_bounds__(kPT, 2) decode_unit_kernel(const StepArgs a) {
         return m;
     };
     RMeta ring{INT_MIN, 0.f, 0.f, -1, 0, make_uint2(0u, 0u)};
-    if (warp == kIssueWarp) ring = load_meta(lane);
 
-    // Programmatic dependent launch: everything above touches only this
-    // call's inputs (slot indices, gates, the pool's block table), which no
-    // earlier decode step writes, so it overlaps the previous kernel's tail.
-    // From here on the pool, q/k/v and out are read or written: wait until the
-    // grids this launch depends on have completed and their writes are
-    // visible.  The next launch on the stream may start its own prologue now.
+    // Programmatic dependent launch: everything above touches nothing in
+    // memory, so it overlaps the previous kernel's tail.  From here on the
+    // pool and the call's tensors (slot indices and gates too: a batch plan or
+    // any other kernel on the stream may have just written them) are read or
+    // written: wait until the grids this launch depends on have completed and
+    // their writes are visible.  The next launch on the stream may start its
+    // own prologue now.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == kIssueWarp) ring = load_meta(lane);
 
     // The refill warp's part of item il: the stage's metadata, the block and
     // the head's row directory (bulk copies completing on the stage's
