@@ -821,14 +821,21 @@ class DampPool:
         f = damp_decode_step_validated if check_inputs else damp_decode_step
         f(self.handle, slot_idx, q, k, v, alpha, beta, out, stream)
 
+    def _on_my_device(self, q):
+        """The kernels run on the tensors' device and may reach the pool's memory from there alone."""
+        if isinstance(q, torch.Tensor) and q.device != self.buf.device:
+            raise ValueError(f"tensors on {q.device}, the pool on {self.buf.device}")
+
     def decay_step(self, slot_idx, q, k, v, alpha, out, stream=None):
         """One token of the decay rule (damp_decay_step)."""
+        self._on_my_device(q)
         damp_decay_step(self.handle, slot_idx, q, k, v, alpha, out, stream)
 
     def prefill(self, plan, q, k, v, alpha, beta=None, out=None, rule="delta", workspace=None,
                 stream=None) -> torch.Tensor:
         """The prompts of a built BatchPlan through one layer (damp_prefill);
         returns ``out`` (allocated, zero-filled, when None)."""
+        self._on_my_device(q)
         if isinstance(q, torch.Tensor) and q.dim() == 3 and q.shape[0] != plan.max_tokens:
             raise ValueError(f"the plan is for {plan.max_tokens} token rows, got {q.shape[0]}")
         if not plan.built:

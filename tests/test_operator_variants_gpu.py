@@ -1,9 +1,10 @@
 """The forms of the decay-rule step and of the token prefill that only larger batches take.  Each case computes
-the rule that chooses its form, so that a change of the rule shows here."""
+the rule that chooses its form, so that a change of the rule shows here.  And a refusal of both operators."""
 import numpy as np
 import pytest
 import torch
 
+import quantized_linear_attention_damp_b200 as D
 from tests import test_decay_step_gpu as step
 from tests import test_prefill_gpu as prefill
 
@@ -63,3 +64,24 @@ def test_prompts_with_32_rows_a_lane(rule, dtype, dk, dv):
     lengths = g.integers(0, 12, n).tolist()
     lengths[5], lengths[9] = 33, 64
     prefill.check(rule, lengths, H=H, Hqk=4, dk=dk, dv=dv, dtype=dtype, past=g.integers(0, 2, n).tolist(), spare=3)
+
+
+def test_tensors_on_another_device_than_the_pool_are_refused():
+    """(The pool's buffer is only said to lie on another device: nothing is launched.)"""
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    n, H, d = 2, 2, 128
+    pool = D.DampPool("int8", n, H, d)
+    one = torch.ones(n, dtype=torch.int32, device="cuda")
+    x, gate = torch.zeros(n, H, d, dtype=torch.bfloat16, device="cuda"), torch.ones(n, H, device="cuda")
+    plan = D.BatchPlan(n, n, n).build(one, torch.arange(n, dtype=torch.int32, device="cuda"))
+    mine, pool.buf = pool.buf, Elsewhere
+    with pytest.raises(ValueError, match="the pool on cuda:1"):
+        pool.prefill(plan, x, x, x, gate, gate)
+    with pytest.raises(ValueError, match="the pool on cuda:1"):
+        pool.decay_step(one - 1, x, x, x, gate, torch.zeros(n, H, d, device="cuda"))
+    pool.buf = mine
+    pool.prefill(plan, x, x, x, gate, gate)
+    assert pool.get_error() == 0
+    pool.close()
