@@ -4,9 +4,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 import quantized_linear_attention_damp_b200 as D
 from tests import test_decay_step_gpu as step
 from tests import test_prefill_gpu as prefill
+from tests.prefill_helpers import EPS32, decay_step
 
 pytestmark = pytest.mark.gpu
 
@@ -83,5 +85,35 @@ def test_tensors_on_another_device_than_the_pool_are_refused():
         pool.decay_step(one - 1, x, x, x, gate, torch.zeros(n, H, d, device="cuda"))
     pool.buf = mine
     pool.prefill(plan, x, x, x, gate, gate)
+    assert pool.get_error() == 0
+    pool.close()
+
+
+@pytest.mark.parametrize("dk,dv,n,H", [(128, 128, 3, 6), (64, 64, 3, 6), (96, 160, 3, 6), (32, 48, 420, 6), (16, 16, 5, 6)])
+def test_step_of_pools_whose_heads_differ(dk, dv, n, H):
+    """A per-head map: no FP16 row at all, one, all of them, and counts that fill no batch of 8."""
+    g = np.random.default_rng(dk)
+    counts = [0, 1, dk, dk - 1, dk // 2 + 3, 5]
+    is16 = np.zeros((H, dk), np.uint8)
+    for h, c in enumerate(counts):
+        is16[h, g.permutation(dk)[:c]] = 1
+    pool = D.DampPool("mixed", n, H, dk, d_v=dv, fp16_map=is16)
+    S0 = g.standard_normal((n, H, dk, dv)).astype(np.float32)
+    slot = g.permutation(n).astype(np.int32)
+    pool.pack(torch.arange(n, dtype=torch.int32, device="cuda"), torch.from_numpy(S0).cuda())
+    st = O.pack(O.FMT_QUANT, is16[None], S0)
+    x = [torch.from_numpy(g.standard_normal((n, H, d)).astype(np.float32)).bfloat16() for d in (dk, dk, dv)]
+    alpha = g.uniform(0.3, 1.0, (n, H)).astype(np.float32)
+    out = torch.empty(n, H, dv, device="cuda")
+    pool.decay_step(torch.from_numpy(slot).cuda(), *(t.cuda() for t in x), torch.from_numpy(alpha).cuda(), out)
+    got, (q, k, v) = out.cpu().numpy().astype(np.float64), (t.float().numpy() for t in x)
+    for b, s in enumerate(slot):
+        want, new, X = decay_step(O.FMT_QUANT, is16, st[int(s)], q[b], k[b], v[b], alpha[b])
+        for name in ("scale", "half", "code"):
+            getattr(st, name)[int(s)] = getattr(new, name)
+        # d_k rounded products and sums, each at most half an FP32 step of the running sum
+        assert (np.abs(got[b] - want) <= (dk + 2) * EPS32 * (np.abs(q[b])[..., None] * np.abs(X)).sum(axis=-2)).all()
+    for name, a in pool.read_logical().items():
+        assert np.array_equal(a, getattr(st, name)), name
     assert pool.get_error() == 0
     pool.close()
