@@ -79,6 +79,25 @@ constexpr int kPrepThreads = 128;
 constexpr int kTile = C * D * 2;       // bytes of a Q, K or V tile: two halves of 64 channels
 constexpr int kHalf = kTile / 2;
 
+// Products of a block's decays up to each of a lane's two tokens, and behind them (a warp; lane l:
+// tokens 2 l and 2 l + 1).  In 64 bits, rounded once: gamma_C multiplies every element of a state, so an
+// error of it is the same for all of them, and where a head's decay does not change it is the same in
+// every block.  (As FP32 products 4096 tokens of such a head came out 7e-5 off, a rounding a block is 2e-6.)
+__device__ __forceinline__ void decay_products(float a0, float a1, int lane, float2& upto, float2& behind) {
+    double up = (double)a0 * a1, down = up;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, up, off), d = __shfl_down_sync(0xffffffffu, down, off);
+        if (lane >= off) up = u * up;
+        if (lane + off < 32) down = down * d;
+    }
+    double before = __shfl_up_sync(0xffffffffu, up, 1), rest = __shfl_down_sync(0xffffffffu, down, 1);
+    if (lane == 0) before = 1.0;
+    if (lane == 31) rest = 1.0;
+    upto = make_float2((float)(before * a0), (float)up);
+    behind = make_float2((float)(a1 * rest), (float)rest);
+}
+
 // Waits for a phase of an mbarrier, at most wait_ns; gives up at once where
 // another warp gave up.  A patient waiter (the loader, whose waits are long
 // and not on the chain) sleeps between its looks: polling takes shared-memory
@@ -189,20 +208,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         const float a1 = i + 1 < len ? __ldg(al + (size_t)(i + 1) * a.H) : 1.f;
         const float b0 = i < len ? __ldg(be + (size_t)i * a.H) : 0.f;
         const float b1 = i + 1 < len ? __ldg(be + (size_t)(i + 1) * a.H) : 0.f;
-        float up = a0 * a1, down = up;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, up, off), d = __shfl_down_sync(0xffffffffu, down, off);
-            if (lane >= off) up = u * up;
-            if (lane + off < 32) down = down * d;
-        }
-        float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-        if (lane == 0) before = 1.f;
-        if (lane == 31) behind = 1.f;
         reinterpret_cast<float2*>(s_al)[lane] = make_float2(a0, a1);
         reinterpret_cast<float2*>(s_be)[lane] = make_float2(b0, b1);
-        reinterpret_cast<float2*>(s_ga)[lane] = make_float2(before * a0, up);
-        reinterpret_cast<float2*>(s_w)[lane] = make_float2(a1 * behind, behind);
+        decay_products(a0, a1, lane, reinterpret_cast<float2*>(s_ga)[lane], reinterpret_cast<float2*>(s_w)[lane]);
     }
     tc_fence_before();
     __syncthreads();
@@ -1045,7 +1053,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
                         S[i] = __fmaf_rn(g, S[i], parts[(size_t)j * D * D + (size_t)i * D]);
                 }
         }
-        float total = 1.f;
+        double total = 1.0;
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
             if (!SUM) {
@@ -1082,7 +1090,7 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             if (SUM) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) parts[(size_t)seg * D * D + (size_t)i * D] = S[i];
-                if (tid == 0) sa.decay[(size_t)unit * sa.segs + seg] = total;
+                if (tid == 0) sa.decay[(size_t)unit * sa.segs + seg] = (float)total;
             } else if (last) {
                 float* to = reinterpret_cast<float*>(
                     states + (size_t)(a.state_by_slot ? slot : req) * a.state_stride) + at;
@@ -1251,22 +1259,9 @@ __global__ void __launch_bounds__(EChain::threads, 1)
         float a0 = alpha_of(2 * lane), a1 = alpha_of(2 * lane + 1);    // of this lane's two tokens
         for (int c = 0; c < nc; ++c) {
             const uint32_t f = bar(X::Full + c % X::kStages);
-            if (c >= X::kStages) {
-                if (!wait_all(X::Empty + c % X::kStages, (c / X::kStages - 1) & 1)) break;
-                if (elect_one()) load(c);
-                issued = c + 1;
-            }
-            // products of the decays up to each token, and behind it
-            float up = a0 * a1, down = up;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, up, off), w = __shfl_down_sync(0xffffffffu, down, off);
-                if (lane >= off) up = u * up;
-                if (lane + off < 32) down = down * w;
-            }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 1.f;
-            if (lane == 31) behind = 1.f;
+            // the products first: they take their time while the stage is still in use
+            float2 upto, behind;
+            decay_products(a0, a1, lane, upto, behind);
             float mid = a0 * a1;               // from token 32 on
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) {
@@ -1275,15 +1270,21 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             }
             float mid0 = __shfl_up_sync(0xffffffffu, mid, 1);
             mid0 = lane == 16 ? a0 : mid0 * a0;
+            const float2 al = make_float2(a0, a1);
+            a0 = alpha_of((c + 1) * C + 2 * lane);
+            a1 = alpha_of((c + 1) * C + 2 * lane + 1);
+            if (c >= X::kStages) {
+                if (!wait_all(X::Empty + c % X::kStages, (c / X::kStages - 1) & 1)) break;
+                if (elect_one()) load(c);
+                issued = c + 1;
+            }
             float2* r = reinterpret_cast<float2*>(ring(c)) + lane;
-            r[0] = make_float2(a0, a1);
-            r[C / 2] = make_float2(before * a0, up);
-            r[C] = make_float2(a1 * behind, behind);
+            r[0] = al;
+            r[C / 2] = upto;
+            r[C] = behind;
             r[3 * C / 2] = make_float2(mid0, mid);
             __syncwarp();
             if (lane == 0) mbar_arrive(f);
-            a0 = alpha_of((c + 1) * C + 2 * lane);
-            a1 = alpha_of((c + 1) * C + 2 * lane + 1);
         }
         // copies in flight end before the CTA does
         for (int c = max(0, issued - X::kStages); c < issued; ++c)

@@ -114,3 +114,28 @@ def test_states_are_as_good_as_fp32_sums(rule, name, past):
         assert ((out[at:at + L].double() - o).abs() <= EPS_BF16 * o.abs() + room).all()
         at += L
     assert max(worst) <= 1.0, worst
+
+
+@pytest.mark.parametrize("rule", ["decay", "delta"])
+@pytest.mark.parametrize("L,H", [(64, 32), (4096, 32), (4000, 100), (9000, 3)])
+def test_constant_decays_over_long_prompts(rule, L, H):
+    """Without keys a state is its first one times the product of all decays.  A head's decay is the same for every
+    token, so every block's product is off by the same amount: one rounding of it and one of the state's update a
+    block are what FP32 allows.  (Few heads: the decay rule cuts the request into segments.)"""
+    g = torch.Generator().manual_seed(L)
+    a = 1 - 0.5 ** (8 + 6 * torch.rand(H, generator=g, dtype=torch.float64))
+    a = a.float()
+    S0 = torch.randn(1, H, 128, 128, generator=g).cuda()
+    zero = torch.zeros(L, H, 128, dtype=torch.bfloat16, device="cuda")
+    v, beta = torch.ones_like(zero), torch.ones(L, H, device="cuda")
+    pool = D.DampPool("fp32", 1, H, 128)
+    pool.pack(i32([0]), S0)
+    plan = D.BatchPlan(1, L, 1).build(i32([L]), i32([0]), i32([1]))
+    pool.prefill(plan, zero, zero, v, a.expand(L, H).contiguous().cuda(), beta if rule == "delta" else None, rule=rule)
+    S1 = torch.empty_like(S0)
+    pool.unpack(i32([0]), S1)
+    assert pool.get_error() == 0
+    pool.close()
+    want = (a.double() ** L).cuda()[:, None, None] * S0[0].double()
+    err = (S1[0].double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    assert (err <= 2 * -(-L // B) * EPS32).all(), err.max()
