@@ -257,6 +257,7 @@ int damp_decay_step(const damp_pool* pool, int n, const int32_t* slot_idx, int i
  *   lengths  : device int32 [n], tokens of each request in this batch (0: none)
  *   past     : device int32 [n] or NULL (all zero): tokens already in the
  *              request's state.  0: the request starts from a zero state.
+ *              past + length below 2^31.
  *   slot_idx : device int32 [n], the pool slot of each request's state; < 0:
  *              padding.  Distinct where >= 0.
  *   max_tokens : token rows of the batch's tensors
@@ -298,7 +299,8 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
 /*
  * The prompts of a planned batch through one layer: every token's readout, and
  * every request's state left in its pool slot, ready for damp_decode_step
- * (DAMP_RULE_DELTA) or damp_decay_step (DAMP_RULE_DECAY).
+ * (DAMP_RULE_DELTA; it takes q and k of every value head, shared ones repeated)
+ * or damp_decay_step (DAMP_RULE_DECAY).
  *   n, max_tokens, cu_seqlens, load_slot, store_slot, block_table, order : the
  *           plan (order: a permutation of the requests, the order in which their
  *           work is started; NULL: as they come)
@@ -326,8 +328,8 @@ int damp_batch_plan(int n, const int32_t* lengths, const int32_t* past, const in
  * with d_k = d_v = 128 run in blocks of 64 tokens on the tensor cores.  There a
  * state is as good as FP32 sums of the block form: a few 1e-6 of its norm or less
  * for the decay rule and for the delta rule with keys in many directions, up to
- * 4e-5 where the keys of a block are all equal up to their sign and beta |k|^2
- * nears 2 (beyond 2 the recurrence itself grows without bound).  The FP32
+ * 5e-5 where the keys of a block are all equal up to their sign and beta |k|^2
+ * nears 2 (beyond 2, without decay, the recurrence itself grows without bound).  The FP32
  * operands of products that only a readout is made of enter as two bf16 values,
  * which lose up to 2^-17 of them; the readout is rounded to bf16 behind that.
  * The same call gives the same bits.

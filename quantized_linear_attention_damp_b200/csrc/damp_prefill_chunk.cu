@@ -127,6 +127,7 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint
 // Q K^T (warps 0, 1) or K K^T (warps 2, 3) and multiplies the decays up along it.
 // The inverse is FP32 arithmetic of the ordinary kind: an error of it is an error
 // of the state.  Q and K share their 32 KB with A and T (FP32) and then with T'.
+// (8672 units: 157 us, 38 % of the issue slots, DRAM 44 %, tensor pipe 5 %.)
 
 // The record of one (block, head): C x C bf16 matrices with 128-byte rows
 // (K-major, 128-byte swizzle) as the chain's products take them, gamma_t
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             }
             uint32_t x[16];
             // (the decays of R behind the wait, the factors of U ahead of theirs, as measured: with both
-            // ahead a thread's registers do not suffice, 450 us against 418 for 8192 tokens x 32 heads)
+            // ahead a thread's registers do not suffice, 579 us against 551 for 8192 tokens x 32 heads)
             if (!(ok = wait_group(warp == 0, X::BK, ph, 4, X::kWarps * 32))) break;
             tc_fence_after();
             tmem_ld16(lanes + X::KS + part * 16, x);
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(DChain::threads, 1)
             if (!wait_group(warp == X::kWarps, X::BO, c & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             // out of TMEM first: the next block's Q S waits for that
-#pragma unroll 1
+#pragma unroll
             for (int part = 0; part < 4; ++part) {
                 uint32_t o1[16], o2[16];
                 tmem_ld16(lanes + X::QS + part * 16, o1);
@@ -1208,11 +1209,9 @@ __global__ void __launch_bounds__(EChain::threads, 1)
             if (!wait_group(warp == X::wOut, X::BO + (c & 1), (c >> 1) & 1, 1, X::kOut * 32)) break;
             tc_fence_after();
             const int live = min(C, len - c * C);
-            // (Not unrolled, as other long loops of this kernel are not: two SMs share an instruction
-            // cache that the unrolled roles together do not fit.  16 ragged requests of 8192 tokens,
-            // 32 heads: 131 us unrolled, 125 so.  The delta chain's roles wait for one another most of
-            // the time, and only its readout is better off: with its other loops not unrolled either,
-            // 8192 tokens x 32 heads took 460 us against 430.)
+            // (Not unrolled, as other long loops of this kernel are not: while all of them were, its warps were
+            // stalled for want of an instruction 2.1 times an issue, now 0.5 times, and the 16 requests took 5 %
+            // longer.  Unrolling this one alone makes no difference, 127 and 128 us.)
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
 #pragma unroll 1
@@ -1237,8 +1236,8 @@ __global__ void __launch_bounds__(EChain::threads, 1)
                         *reinterpret_cast<uint16_t*>(to + X::out_row) = (uint16_t)(o >> 16);
                     }
                 }
-                // (rows of 256 bytes from shared memory: a warp's own 64 bytes of each, as they come, took 156 us
-                // for the 16 requests)
+                // (rows of 256 bytes from shared memory: a warp's own 64 bytes of each, as they come, took 157 us
+                // for the 16 requests against 126)
                 bar_sync(1, X::kOut * 32);
 #pragma unroll
                 for (int i = 0; i < C / 2 * 16 / (X::kOut * 32); ++i) {
@@ -1394,8 +1393,8 @@ cudaError_t token_map(CUtensorMap* m, const void* p, int heads, long long rows, 
 // Segments of a request for the decay rule: as many as the SMs have room for,
 // none shorter (on average) than 4 blocks; a batch whose (request, head) pairs
 // take more than half of the SMs stays whole (the first pass reads K and V once
-// more).  One prompt of 4096 tokens x 32 heads: 74 us in 4 segments, 119 in 2,
-// 158 whole.
+// more).  One prompt of 4096 tokens x 32 heads: 89 us in 4 segments, 145 in 2,
+// 185 whole.
 int decay_segments(int n, int H, int max_tokens, int sms) {
     const long long chains = (long long)n * H;
     if (chains * 2 > sms) return 1;
