@@ -49,9 +49,11 @@ PROFILE_DIR = os.path.join(ROOT, "profiles")
 
 def unit_bytes(w: W.Workload, fmt: str) -> int:
     """Algorithmic bytes of one (slot, head) step: state read + write, q, k, v,
-    alpha, beta, out (block padding excluded)."""
-    import quantized_linear_attention_damp_b200 as D
-    block, _ = D.damp_layout(D.FORMATS[fmt], w.d, w.d, w.hp if fmt == "mixed" else 0)
+    alpha, beta, out (block padding excluded).  The block's size is worked out
+    here, for the reference arm loads nothing of the library."""
+    r16 = w.hp if fmt == "mixed" else 0
+    # FP16 rows, and byte rows with an FP32 scale each
+    block = 4 * w.d * w.d if fmt == "fp32" else 2 * r16 * w.d + (w.d - r16) * (w.d + 4)
     elt = 2 if w.in_dtype == "bf16" else 4
     alpha = 4 * w.d if w.gate == W.GATE_KDA else 4
     return 2 * block + 3 * w.d * elt + alpha + 4 + 4 * w.d
